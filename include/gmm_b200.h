@@ -389,6 +389,126 @@ gmm_status kmeans_step(const void *X, gmm_dtype dtype, int B, int64_t N, int d, 
                        int32_t *counts, double *inertia,
                        void *ws, size_t ws_bytes, uint32_t flags, void *stream);
 
+/* --------------------------------------------------------------- experts */
+
+/*
+ * Mixtures of experts on the components of a soft (or hard) assignment:
+ * every point passes through the maps of the components gmm_soft_assign (or
+ * a k-means step, r = 1) gave it, and the results are added up by weight.
+ * With e = ids_ni, g_ni = resp_ni (1 when resp is NULL), f the activation:
+ *
+ *   gmm_expert_linear   y_n = sum_i g_ni f(W_e x_n + b_e) + residual_n
+ *   gmm_expert_mlp      y_n = sum_i g_ni (W2_e h_ni + b2_e) + residual_n,
+ *                       h_ni = f(W1_e x_n + b1_e), or, gated,
+ *                       h_ni = f(a) * u with (a, u) the first and the last h
+ *                       rows of W1_e x_n + b1_e
+ *
+ * Entries with ids_ni < 0 are skipped (a point without any gives
+ * residual_n, or 0); one with ids_ni >= K is skipped too and records
+ * GMM_ERR_RANGE in the error word.  The same component may be listed twice.
+ * Without ids (NULL, r = 0, K = 1) every point passes through the one map:
+ * a dense layer, f(X W^T + b) + residual.
+ *
+ * Sums are fp32 (tensor-core accumulators, or FMA).  Results are rounded to
+ * `dtype` once; for 16-bit types the hidden vector h and, in the backward
+ * pass, the gradients of the pre-activations and g h are rounded to `dtype`
+ * as well, because they are operands of the next tensor-core product.  Every
+ * sum has a fixed order: results are bitwise reproducible.
+ *
+ * The kernels, by sizes and types (gmm_expert_path):
+ *   2  16-bit types, d, h and o multiples of 8, X, dY and weights 16-byte
+ *      aligned: grouped products on the tensor cores (tcgen05);
+ *   1  the same with few points (GMM_EXPERT_FEW_PAIRS pairs at most, forward
+ *      only): kernels that stream each used expert's weights once;
+ *   0  everything else (fp32, odd sizes) and GMM_FLAG_FORCE_SIMT: CUDA cores.
+ */
+typedef enum gmm_activation {
+    GMM_ACT_NONE = 0,
+    GMM_ACT_RELU = 1,
+    GMM_ACT_GELU = 2,  /* z Phi(z), Phi the normal distribution function */
+    GMM_ACT_SILU = 3   /* z / (1 + exp(-z)) */
+} gmm_activation;
+
+typedef struct gmm_expert_shape {
+    int64_t N;           /* points, >= 1 */
+    int32_t d;           /* input width, 1..GMM_EXPERT_MAX_DIM */
+    int32_t h;           /* hidden width of gmm_expert_mlp; 0 for gmm_expert_linear */
+    int32_t o;           /* output width */
+    int32_t K;           /* experts, 1..GMM_EXPERT_MAX_K */
+    int32_t r;           /* entries per point, 1..8; 0 = dense (K = 1, no ids) */
+    int32_t dtype;       /* gmm_dtype of X, weights, biases, residual, Y */
+    int32_t activation;  /* gmm_activation */
+    int32_t gated;       /* gmm_expert_mlp: 1 = gated; otherwise 0 */
+} gmm_expert_shape;
+
+#define GMM_EXPERT_MAX_DIM 32768
+#define GMM_EXPERT_MAX_K 4096
+#define GMM_EXPERT_FEW_PAIRS 256
+
+/*
+ * Which kernels a call with this shape runs (see above; aligned pointers
+ * assumed), or -1 for an invalid shape.
+ */
+int gmm_expert_path(const gmm_expert_shape *shape, int backward, uint32_t flags);
+
+/*
+ * Bytes of device workspace the forward (backward = 0) or backward
+ * (backward = 1) call of this shape needs with these flags (0 for an invalid
+ * shape).  A workspace of the backward call serves the forward call too.
+ * Clear its error word once with gmm_workspace_init.
+ */
+size_t gmm_expert_workspace_size(const gmm_expert_shape *shape, int backward, uint32_t flags);
+
+/*
+ *   X        [N x d], W [K x o x d], b [K x o] or NULL, residual [N x o] or
+ *            NULL, Y [N x o], all row-major contiguous in shape->dtype.
+ *   ids      [N x r] int32, or NULL when r = 0.
+ *   resp     [N x r] fp32, or NULL (all weights 1).
+ *   Y may be the residual's own buffer; it may not overlap another input.
+ *   flags    0, or GMM_FLAG_FORCE_SIMT (CUDA-core kernels).
+ * Errors: GMM_ERR_INVALID_ARG for NULL or misaligned pointers (X, weights,
+ * Y, dY and the gradients of X and the weights 16 bytes, the workspace 256,
+ * the others their element), invalid shapes and flags, a short workspace;
+ * GMM_ERR_CUDA if a launch fails.  Nothing is launched then.
+ */
+gmm_status gmm_expert_linear(const gmm_expert_shape *shape, const void *X, const int32_t *ids,
+                             const float *resp, const void *W, const void *b,
+                             const void *residual, void *Y, void *ws, size_t ws_bytes,
+                             uint32_t flags, void *stream);
+
+/*
+ * The gradients of every input of gmm_expert_linear for dY = dL/dY:
+ *   dX [N x d], dW [K x o x d], db [K x o] (NULL iff b is NULL) in
+ *   shape->dtype, dresp [N x r] fp32 (NULL iff resp is NULL; 0 for skipped
+ *   entries).  The residual's gradient is dY.  dX, dW are written whole
+ *   (zeros for experts and points without entries).
+ */
+gmm_status gmm_expert_linear_backward(const gmm_expert_shape *shape, const void *dY,
+                                      const void *X, const int32_t *ids, const float *resp,
+                                      const void *W, const void *b, void *dX, void *dW, void *db,
+                                      float *dresp, void *ws, size_t ws_bytes, uint32_t flags,
+                                      void *stream);
+
+/*
+ *   W1 [K x (gated ? 2h : h) x d], b1 [K x (gated ? 2h : h)] or NULL,
+ *   W2 [K x o x h], b2 [K x o] or NULL; the rest as gmm_expert_linear.
+ */
+gmm_status gmm_expert_mlp(const gmm_expert_shape *shape, const void *X, const int32_t *ids,
+                          const float *resp, const void *W1, const void *b1, const void *W2,
+                          const void *b2, const void *residual, void *Y, void *ws,
+                          size_t ws_bytes, uint32_t flags, void *stream);
+
+/*
+ * The gradients of every input of gmm_expert_mlp.  The hidden
+ * pre-activations are computed again from X, in fp32, so the forward call
+ * keeps nothing.  db1 / db2 are NULL iff b1 / b2 are, dresp iff resp is.
+ */
+gmm_status gmm_expert_mlp_backward(const gmm_expert_shape *shape, const void *dY, const void *X,
+                                   const int32_t *ids, const float *resp, const void *W1,
+                                   const void *b1, const void *W2, const void *b2, void *dX,
+                                   void *dW1, void *db1, void *dW2, void *db2, float *dresp,
+                                   void *ws, size_t ws_bytes, uint32_t flags, void *stream);
+
 /* ---------------------------------------------------------------- errors */
 
 /*

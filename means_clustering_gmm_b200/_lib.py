@@ -66,7 +66,21 @@ SIGNATURES = {
     "gmm_init_kmeans_workspace_size": (_sz, [_i64, _i32, _i32]),
     "gmm_init_kmeans": (_i32, [_vp, _i32, _i64, _i32, _i32, _i32, ctypes.c_float, _vp, _vp, _vp,
                                _vp, _vp, _sz, _vp]),
+    "gmm_expert_path": (_i32, [_vp, _i32, _u32]),
+    "gmm_expert_workspace_size": (_sz, [_vp, _i32, _u32]),
+    "gmm_expert_linear": (_i32, [_vp] * 9 + [_sz, _u32, _vp]),
+    "gmm_expert_linear_backward": (_i32, [_vp] * 12 + [_sz, _u32, _vp]),
+    "gmm_expert_mlp": (_i32, [_vp] * 11 + [_sz, _u32, _vp]),
+    "gmm_expert_mlp_backward": (_i32, [_vp] * 16 + [_sz, _u32, _vp]),
 }
+
+
+
+class ExpertShape(ctypes.Structure):
+    """gmm_expert_shape of include/gmm_b200.h."""
+    _fields_ = [("N", ctypes.c_int64)] + [(n, ctypes.c_int32) for n in (
+        "d", "h", "o", "K", "r", "dtype", "activation", "gated")]
+
 
 _lock = threading.Lock()
 _lib = None

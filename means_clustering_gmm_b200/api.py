@@ -112,6 +112,21 @@ class Workspace:
     def for_kmeans(cls, B, N, d, K, device=None):
         return cls(kmeans_workspace_size(B, N, d, K), device)
 
+    @classmethod
+    def for_expert_linear(cls, N, d, o, K, r, dtype=torch.float32, device=None, backward=False,
+                          flags=GMM_FLAG_NONE):
+        """Workspace of expert_linear (and, with backward, of its gradients);
+        r = 0 is the dense form."""
+        from .experts import expert_workspace_size
+        return cls(expert_workspace_size(N, d, 0, o, K, r, dtype, False, backward, flags), device)
+
+    @classmethod
+    def for_expert_mlp(cls, N, d, h, o, K, r, dtype=torch.float32, device=None, gated=False,
+                       backward=False, flags=GMM_FLAG_NONE):
+        """Workspace of expert_mlp (and, with backward, of its gradients)."""
+        from .experts import expert_workspace_size
+        return cls(expert_workspace_size(N, d, h, o, K, r, dtype, gated, backward, flags), device)
+
 
 def gmm_em_step(X: torch.Tensor, means: torch.Tensor, variances: torch.Tensor,
                 logw: torch.Tensor, ws: Workspace, stats: torch.Tensor | None = None,

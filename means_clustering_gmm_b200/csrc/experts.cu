@@ -1,0 +1,276 @@
+// C ABI of the experts' products (declared in include/gmm_b200.h): argument
+// checks, workspace layout and the order of the launches.
+#include "experts.h"
+
+using namespace gmmb;
+
+namespace {
+
+bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
+
+bool valid_shape(const gmm_expert_shape *s, bool mlp) {
+    if (!s || s->N < 1 || s->d < 1 || s->d > GMM_EXPERT_MAX_DIM || s->o < 1 ||
+        s->o > GMM_EXPERT_MAX_DIM || s->K < 1 || s->K > GMM_EXPERT_MAX_K || s->r < 0 ||
+        s->r > kTopMax)
+        return false;
+    if (mlp ? (s->h < 1 || s->h > GMM_EXPERT_MAX_DIM) : s->h != 0) return false;
+    if (s->dtype != GMM_F32 && s->dtype != GMM_BF16 && s->dtype != GMM_F16) return false;
+    if (s->activation < GMM_ACT_NONE || s->activation > GMM_ACT_SILU) return false;
+    if (s->gated != 0 && (s->gated != 1 || !mlp)) return false;
+    if (s->r == 0 && s->K != 1) return false;
+    // rows are counted in 32 bits, segments rounded up to whole tiles
+    const int64_t rows = ((int64_t)1 << 31) - (int64_t)(GMM_EXPERT_MAX_K + 2) * kExpTile;
+    return s->N <= rows / (s->r ? s->r : 1);
+}
+
+ExpShape make_shape(const gmm_expert_shape *s) {
+    ExpShape p;
+    p.N = s->N;
+    p.P = s->N * (s->r ? s->r : 1);
+    p.d = s->d;
+    p.h = s->h;
+    p.o = s->o;
+    p.K = s->K;
+    p.r = s->r;
+    p.gated = s->gated == 1;
+    p.gh = p.gated ? 2 * p.h : p.h;
+    p.dt = (gmm_dtype)s->dtype;
+    p.act = s->activation;
+    p.mlp = s->h > 0;
+    p.dense = s->r == 0;
+    return p;
+}
+
+int path_of(const ExpShape &, bool, uint32_t) { return 0; }
+
+struct Layout {
+    size_t cnt, seg, tile_expert, ntiles, row_pair, hist, hid, da, slots, rpart, total;
+    int64_t max_rows;
+    int max_tiles, nrpart;
+    size_t esize;
+};
+
+Layout layout_of(const ExpShape &p, bool backward, int path) {
+    Layout L;
+    const int64_t segs = p.dense ? 1 : (p.K + 1 < p.P ? p.K + 1 : p.P);
+    L.max_tiles = (int)((p.P + segs * (kExpTile - 1)) / kExpTile);
+    if (L.max_tiles < 1) L.max_tiles = 1;
+    L.max_rows = (int64_t)L.max_tiles * kExpTile;
+    L.esize = path == 0 ? 4 : 2;
+    const int width = p.mlp ? p.h : p.o;
+    L.nrpart = (width + 63) / 64;
+    size_t o = kAlign;   // error word
+    auto take = [&](size_t &off, size_t bytes) {
+        off = o;
+        o = align_up(o + bytes);
+    };
+    const size_t KK = (size_t)p.K + 1;
+    const size_t chunks = p.dense ? 0 : (size_t)((p.P + 255) / 256);
+    take(L.cnt, p.dense ? 0 : KK * 4);
+    take(L.seg, p.dense ? 0 : (KK + 1) * 4);
+    take(L.tile_expert, p.dense ? 0 : (size_t)L.max_tiles * 4);
+    take(L.ntiles, 4);
+    take(L.row_pair, p.dense ? 0 : (size_t)L.max_rows * 4);
+    take(L.hist, chunks * KK * 4);
+    take(L.hid, p.mlp ? (size_t)L.max_rows * p.h * L.esize : 0);
+    take(L.da, backward ? (size_t)L.max_rows * p.first() * L.esize : 0);
+    const int wide = !backward ? p.o : (p.d > p.o ? p.d : p.o);
+    take(L.slots, p.direct() ? 0 : (size_t)p.P * wide * 4);
+    take(L.rpart, backward ? (size_t)L.max_rows * L.nrpart * 4 : 0);
+    L.total = o;
+    return L;
+}
+
+ExpCall make_call(const ExpShape &p, const Layout &L, void *ws, const int32_t *ids) {
+    ExpCall c = {};
+    char *b = (char *)ws;
+    c.s = p;
+    c.err = (int *)b;
+    c.rt.cnt = (int *)(b + L.cnt);
+    c.rt.seg = (int *)(b + L.seg);
+    c.rt.tile_expert = (int *)(b + L.tile_expert);
+    c.rt.ntiles = (int *)(b + L.ntiles);
+    c.rt.row_pair = (int *)(b + L.row_pair);
+    c.rt.hist = (int *)(b + L.hist);
+    c.rt.ids = ids;
+    c.rt.N = p.N;
+    c.rt.P = p.P;
+    c.rt.K = p.K;
+    c.rt.r = p.r ? p.r : 1;
+    c.rt.max_tiles = L.max_tiles;
+    c.hid = b + L.hid;
+    c.da = b + L.da;
+    c.slots = (float *)(b + L.slots);
+    c.rpart = (float *)(b + L.rpart);
+    c.max_rows = L.max_rows;
+    c.nrpart = L.nrpart;
+    c.esize = L.esize;
+    return c;
+}
+
+bool known_flags(uint32_t flags) { return (flags & ~(uint32_t)GMM_FLAG_FORCE_SIMT) == 0; }
+
+// The checks the four entry points share; `big` arrays are 16-byte aligned,
+// `small` ones to their element.
+struct Checks {
+    bool ok = true;
+    size_t elem;
+    void big(const void *p) { ok = ok && p && aligned(p, 16); }
+    void small(const void *p, size_t a) { ok = ok && (!p || aligned(p, a)); }
+    void routing(const gmm_expert_shape *s, const int32_t *ids, const float *resp) {
+        ok = ok && (ids != nullptr) == (s->r > 0) && (s->r > 0 || !resp);
+        small(ids, 4);
+        small(resp, 4);
+    }
+    void pair(const void *a, const void *grad) {   // an optional input and its gradient
+        ok = ok && (a == nullptr) == (grad == nullptr);
+    }
+    void workspace(const void *ws, size_t have, size_t need) {
+        ok = ok && ws && aligned(ws, kAlign) && have >= need;
+    }
+};
+
+gmm_status forward(const gmm_expert_shape *shape, bool mlp, const void *X, const int32_t *ids,
+                   const float *resp, const void *W1, const void *b1, const void *W2,
+                   const void *b2, const void *residual, void *Y, void *ws, size_t ws_bytes,
+                   uint32_t flags, cudaStream_t s) {
+    if (!valid_shape(shape, mlp) || !known_flags(flags)) return GMM_ERR_INVALID_ARG;
+    const ExpShape p = make_shape(shape);
+    const int path = path_of(p, false, flags);
+    const Layout L = layout_of(p, false, path);
+    Checks k;
+    k.elem = p.dt == GMM_F32 ? 4 : 2;
+    k.big(X);
+    k.big(W1);
+    if (mlp) k.big(W2);
+    k.big(Y);
+    k.small(b1, k.elem);
+    k.small(b2, k.elem);
+    k.small(residual, k.elem);
+    k.routing(shape, ids, resp);
+    k.ok = k.ok && Y != X;
+    k.workspace(ws, ws_bytes, L.total);
+    if (!k.ok) return GMM_ERR_INVALID_ARG;
+    ExpCall c = make_call(p, L, ws, ids);
+    c.x = X;
+    c.w1 = W1;
+    c.b1 = b1;
+    c.w2 = W2;
+    c.b2 = b2;
+    c.res = residual;
+    c.resp = resp;
+    c.y = Y;
+    if (launch_exp_route(c, s) != cudaSuccess) return GMM_ERR_CUDA;
+    if (launch_exp_simt(c, false, s) != cudaSuccess) return GMM_ERR_CUDA;
+    if (!p.direct() && launch_exp_combine(c, false, s) != cudaSuccess) return GMM_ERR_CUDA;
+    return GMM_OK;
+}
+
+gmm_status backward(const gmm_expert_shape *shape, bool mlp, const void *dY, const void *X,
+                    const int32_t *ids, const float *resp, const void *W1, const void *b1,
+                    const void *W2, const void *b2, void *dX, void *dW1, void *db1, void *dW2,
+                    void *db2, float *dresp, void *ws, size_t ws_bytes, uint32_t flags,
+                    cudaStream_t s) {
+    if (!valid_shape(shape, mlp) || !known_flags(flags)) return GMM_ERR_INVALID_ARG;
+    const ExpShape p = make_shape(shape);
+    const int path = path_of(p, true, flags);
+    const Layout L = layout_of(p, true, path);
+    Checks k;
+    k.elem = p.dt == GMM_F32 ? 4 : 2;
+    k.big(dY);
+    k.big(X);
+    k.big(W1);
+    k.big(dX);
+    k.big(dW1);
+    if (mlp) {
+        k.big(W2);
+        k.big(dW2);
+    }
+    k.small(b1, k.elem);
+    k.small(b2, k.elem);
+    k.small(db1, k.elem);
+    k.small(db2, k.elem);
+    k.small(dresp, 4);
+    k.pair(b1, db1);
+    k.pair(b2, db2);
+    k.pair(resp, dresp);
+    k.routing(shape, ids, resp);
+    k.ok = k.ok && dX != X && dX != dY;
+    k.workspace(ws, ws_bytes, L.total);
+    if (!k.ok) return GMM_ERR_INVALID_ARG;
+    ExpCall c = make_call(p, L, ws, ids);
+    c.dy = dY;
+    c.x = X;
+    c.w1 = W1;
+    c.b1 = b1;
+    c.w2 = W2;
+    c.b2 = b2;
+    c.resp = resp;
+    c.dx = dX;
+    c.dw1 = dW1;
+    c.db1 = db1;
+    c.dw2 = dW2;
+    c.db2 = db2;
+    c.dresp = dresp;
+    if (launch_exp_route(c, s) != cudaSuccess) return GMM_ERR_CUDA;
+    if (launch_exp_simt(c, true, s) != cudaSuccess) return GMM_ERR_CUDA;
+    if (!p.direct() && launch_exp_combine(c, true, s) != cudaSuccess) return GMM_ERR_CUDA;
+    if (launch_exp_bias_grads(c, s) != cudaSuccess) return GMM_ERR_CUDA;
+    if (dresp && launch_exp_dresp(c, s) != cudaSuccess) return GMM_ERR_CUDA;
+    return GMM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int gmm_expert_path(const gmm_expert_shape *shape, int backward_call, uint32_t flags) {
+    if (!shape || !valid_shape(shape, shape->h > 0) || !known_flags(flags)) return -1;
+    return path_of(make_shape(shape), backward_call != 0, flags);
+}
+
+size_t gmm_expert_workspace_size(const gmm_expert_shape *shape, int backward_call,
+                                 uint32_t flags) {
+    if (!shape || !valid_shape(shape, shape->h > 0) || !known_flags(flags)) return 0;
+    const ExpShape p = make_shape(shape);
+    const size_t fwd = layout_of(p, false, path_of(p, false, flags)).total;
+    if (!backward_call) return fwd;
+    const size_t bwd = layout_of(p, true, path_of(p, true, flags)).total;
+    return bwd > fwd ? bwd : fwd;
+}
+
+gmm_status gmm_expert_linear(const gmm_expert_shape *shape, const void *X, const int32_t *ids,
+                             const float *resp, const void *W, const void *b,
+                             const void *residual, void *Y, void *ws, size_t ws_bytes,
+                             uint32_t flags, void *stream) {
+    return forward(shape, false, X, ids, resp, W, b, nullptr, nullptr, residual, Y, ws, ws_bytes,
+                   flags, (cudaStream_t)stream);
+}
+
+gmm_status gmm_expert_linear_backward(const gmm_expert_shape *shape, const void *dY,
+                                      const void *X, const int32_t *ids, const float *resp,
+                                      const void *W, const void *b, void *dX, void *dW, void *db,
+                                      float *dresp, void *ws, size_t ws_bytes, uint32_t flags,
+                                      void *stream) {
+    return backward(shape, false, dY, X, ids, resp, W, b, nullptr, nullptr, dX, dW, db, nullptr,
+                    nullptr, dresp, ws, ws_bytes, flags, (cudaStream_t)stream);
+}
+
+gmm_status gmm_expert_mlp(const gmm_expert_shape *shape, const void *X, const int32_t *ids,
+                          const float *resp, const void *W1, const void *b1, const void *W2,
+                          const void *b2, const void *residual, void *Y, void *ws,
+                          size_t ws_bytes, uint32_t flags, void *stream) {
+    return forward(shape, true, X, ids, resp, W1, b1, W2, b2, residual, Y, ws, ws_bytes, flags,
+                   (cudaStream_t)stream);
+}
+
+gmm_status gmm_expert_mlp_backward(const gmm_expert_shape *shape, const void *dY, const void *X,
+                                   const int32_t *ids, const float *resp, const void *W1,
+                                   const void *b1, const void *W2, const void *b2, void *dX,
+                                   void *dW1, void *db1, void *dW2, void *db2, float *dresp,
+                                   void *ws, size_t ws_bytes, uint32_t flags, void *stream) {
+    return backward(shape, true, dY, X, ids, resp, W1, b1, W2, b2, dX, dW1, db1, dW2, db2, dresp,
+                    ws, ws_bytes, flags, (cudaStream_t)stream);
+}
+
+}  // extern "C"

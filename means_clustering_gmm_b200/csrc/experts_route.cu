@@ -1,0 +1,317 @@
+// Routing of the experts' products and the sums around them.
+//
+// Routing is a stable counting sort of the (point, entry) pairs by expert,
+// as the k-means update sorts points by cluster: histograms of chunks of 256
+// pairs (one warp each), a scan over the chunks per expert, a scan over the
+// experts with every segment rounded up to whole 128-row tiles, a stable
+// scatter.  No floating-point atomics and no order that depends on
+// scheduling, so every later sum over a segment is reproducible.
+#include "experts.h"
+
+namespace gmmb {
+
+constexpr int kChunkPairs = 256;   // pairs per warp of the sort
+
+// Key of a pair: its expert, or K where it has none.
+__device__ __forceinline__ int pair_key(const int32_t *ids, int64_t p, int K, int *err) {
+    const int id = ids[p];
+    if (id >= K) set_error(err, GMM_ERR_RANGE);
+    return id < 0 || id >= K ? K : id;
+}
+
+__global__ void __launch_bounds__(128)
+exp_hist_kernel(ExpRoute rt, int *err) {
+    extern __shared__ int sh[];
+    const int KK = rt.K + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int *row = sh + warp * KK;
+    const int64_t chunk = (int64_t)blockIdx.x * 4 + warp;
+    const int64_t p0 = chunk * kChunkPairs;
+    if (p0 >= rt.P) return;
+    for (int e = lane; e < KK; e += 32) row[e] = 0;
+    __syncwarp();
+    for (int i = 0; i < kChunkPairs; i += 32) {
+        const int64_t p = p0 + i + lane;
+        const int key = p < rt.P ? pair_key(rt.ids, p, rt.K, err) : -1;
+        const unsigned same = __match_any_sync(0xffffffffu, key);
+        if (key >= 0 && lane == __ffs(same) - 1) row[key] += __popc(same);
+        __syncwarp();
+    }
+    for (int e = lane; e < KK; e += 32) rt.hist[chunk * KK + e] = row[e];
+}
+
+// One warp per key: exclusive scan of its counts over the chunks, in place.
+__global__ void __launch_bounds__(128)
+exp_scan_kernel(ExpRoute rt, int64_t nch) {
+    const int KK = rt.K + 1, lane = threadIdx.x & 31;
+    const int e = blockIdx.x * 4 + (threadIdx.x >> 5);
+    if (e >= KK) return;
+    int total = 0;
+    for (int64_t c0 = 0; c0 < nch; c0 += 32) {
+        const int64_t c = c0 + lane;
+        const int v = c < nch ? rt.hist[c * KK + e] : 0;
+        int x = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        if (c < nch) rt.hist[c * KK + e] = total + x - v;
+        total += __shfl_sync(0xffffffffu, x, 31);
+    }
+    // points without an expert make rows only where the last product writes
+    // the result itself
+    if (lane == 0) rt.cnt[e] = e < rt.K || rt.r <= 1 ? total : 0;
+}
+
+// One block: segment starts (whole tiles) and the expert of every tile.
+__global__ void __launch_bounds__(1024)
+exp_tiles_kernel(ExpRoute rt) {
+    extern __shared__ int sh[];   // [KK + 1] first tile of each segment
+    __shared__ int wsum[32];
+    const int KK = rt.K + 1, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (KK + 1023) / 1024;
+    int mine = 0;
+    for (int i = 0; i < per; ++i) {
+        const int e = tid * per + i;
+        if (e < KK) mine += (rt.cnt[e] + kExpTile - 1) / kExpTile;
+    }
+    int x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) wsum[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+        int w = wsum[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, w, o);
+            if (lane >= o) w += y;
+        }
+        wsum[lane] = w;
+    }
+    __syncthreads();
+    int t = x - mine + (warp ? wsum[warp - 1] : 0);
+    for (int i = 0; i < per; ++i) {
+        const int e = tid * per + i;
+        if (e < KK) {
+            sh[e] = t;
+            rt.seg[e] = t * kExpTile;
+            t += (rt.cnt[e] + kExpTile - 1) / kExpTile;
+        }
+    }
+    const int total = wsum[31];
+    if (tid == 0) {
+        sh[KK] = total;
+        rt.seg[KK] = total * kExpTile;
+        rt.ntiles[0] = total;
+    }
+    __syncthreads();
+    for (int i = tid; i < total; i += 1024) {
+        int lo = 0, hi = KK;   // last e with sh[e] <= i
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (sh[mid] <= i) lo = mid; else hi = mid;
+        }
+        rt.tile_expert[i] = lo;
+    }
+}
+
+__global__ void __launch_bounds__(128)
+exp_scatter_kernel(ExpRoute rt) {
+    extern __shared__ int sh[];
+    const int KK = rt.K + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int *row = sh + warp * KK;   // next row of each expert for this chunk
+    const int64_t chunk = (int64_t)blockIdx.x * 4 + warp;
+    const int64_t p0 = chunk * kChunkPairs;
+    if (p0 >= rt.P) return;
+    for (int e = lane; e < KK; e += 32) row[e] = rt.seg[e] + rt.hist[chunk * KK + e];
+    __syncwarp();
+    for (int i = 0; i < kChunkPairs; i += 32) {
+        const int64_t p = p0 + i + lane;
+        int key = -1;
+        if (p < rt.P) key = pair_key(rt.ids, p, rt.K, nullptr);
+        if (key == rt.K && rt.r > 1) key = -1;
+        const unsigned same = __match_any_sync(0xffffffffu, key);
+        const int rank = __popc(same & ((1u << lane) - 1));
+        const int base = key >= 0 ? row[key] : 0;
+        __syncwarp();
+        if (key >= 0) {
+            rt.row_pair[base + rank] = (int)p;
+            if (rank == 0) row[key] = base + __popc(same);
+        }
+        __syncwarp();
+    }
+}
+
+cudaError_t launch_exp_route(const ExpCall &c, cudaStream_t s) {
+    const ExpRoute &rt = c.rt;
+    if (!rt.ids) return cudaSuccess;
+    const int KK = rt.K + 1;
+    const int64_t nch = (rt.P + kChunkPairs - 1) / kChunkPairs;
+    const unsigned blocks = (unsigned)((nch + 3) / 4);
+    const int smem = 4 * KK * (int)sizeof(int);
+    cudaError_t e;
+    if (smem > 48 * 1024) {
+        e = cudaFuncSetAttribute(exp_hist_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        e = cudaFuncSetAttribute(exp_scatter_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 smem);
+        if (e != cudaSuccess) return e;
+    }
+    exp_hist_kernel<<<blocks, 128, smem, s>>>(rt, c.err);
+    exp_scan_kernel<<<(KK + 3) / 4, 128, 0, s>>>(rt, nch);
+    exp_tiles_kernel<<<1, 1024, (KK + 1) * sizeof(int), s>>>(rt);
+    exp_scatter_kernel<<<blocks, 128, smem, s>>>(rt);
+    note_launches(4);
+    return cudaGetLastError();
+}
+
+// ------------------------------------------------------------- combine
+// One thread per output element (columns fastest): reads r rows of slots and
+// writes one result; bound by HBM.
+template <typename T, bool BWD>
+__global__ void __launch_bounds__(256)
+exp_combine_kernel(ExpRoute rt, const float *__restrict__ slots, const float *__restrict__ resp,
+                   const T *res, T *out, int width) {
+    const int col = blockIdx.x * 256 + threadIdx.x;
+    if (col >= width) return;
+    for (int64_t n = blockIdx.y; n < rt.N; n += gridDim.y) {
+        float acc = 0.f;
+        for (int i = 0; i < rt.r; ++i) {
+            const int64_t p = n * rt.r + i;
+            if (!rt.used(p)) continue;
+            const float v = slots[p * width + col];
+            acc = BWD ? acc + v : fmaf(resp ? resp[p] : 1.f, v, acc);
+        }
+        if (!BWD && res) acc += to_float(res[n * width + col]);
+        out[n * width + col] = from_float<T>(acc);
+    }
+}
+
+template <typename T> static void combine_t(const ExpCall &c, bool backward, cudaStream_t s) {
+    const int width = backward ? c.s.d : c.s.o;
+    const dim3 grid((width + 255) / 256, (unsigned)(c.s.N < 32768 ? c.s.N : 32768));
+    if (backward)
+        exp_combine_kernel<T, true><<<grid, 256, 0, s>>>(c.rt, c.slots, nullptr, nullptr,
+                                                         (T *)c.dx, width);
+    else
+        exp_combine_kernel<T, false><<<grid, 256, 0, s>>>(c.rt, c.slots, c.resp, (const T *)c.res,
+                                                          (T *)c.y, width);
+}
+
+cudaError_t launch_exp_combine(const ExpCall &c, bool backward, cudaStream_t s) {
+    switch (c.s.dt) {
+        case GMM_F32: combine_t<float>(c, backward, s); break;
+        case GMM_BF16: combine_t<__nv_bfloat16>(c, backward, s); break;
+        default: combine_t<__half>(c, backward, s);
+    }
+    note_launches(1);
+    return cudaGetLastError();
+}
+
+// --------------------------------------------------------------- dresp
+// One warp per row: the row's partial sums in order, then <dy, b2>.
+template <typename T>
+__global__ void __launch_bounds__(256)
+exp_dresp_kernel(ExpRoute rt, const float *__restrict__ part, int nparts, const T *__restrict__ dy,
+                 const T *__restrict__ b2, int o, float *__restrict__ dresp) {
+    const int lane = threadIdx.x & 31;
+    const int64_t rows = (int64_t)rt.tiles() * kExpTile;
+    for (int64_t row = blockIdx.x * 8 + (threadIdx.x >> 5); row < rows; row += gridDim.x * 8) {
+        const auto t = rt.tile((int)(row / kExpTile));
+        if (row >= t.seg_end || t.expert >= rt.K) continue;
+        const int64_t p = rt.pair(row);
+        float acc = 0.f;
+        for (int i = lane; i < nparts; i += 32) acc += part[row * nparts + i];
+        if (b2) {
+            const T *g = dy + rt.token(p) * o, *b = b2 + (size_t)t.expert * o;
+            for (int i = lane; i < o; i += 32) acc = fmaf(to_float(g[i]), to_float(b[i]), acc);
+        }
+#pragma unroll
+        for (int m = 16; m; m >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, m);
+        if (lane == 0) dresp[p] = acc;
+    }
+}
+
+template <typename T> static void dresp_t(const ExpCall &c, cudaStream_t s) {
+    exp_dresp_kernel<T><<<148 * 8, 256, 0, s>>>(c.rt, c.rpart, c.nrpart, (const T *)c.dy,
+                                                (const T *)c.b2, c.s.o, c.dresp);
+}
+
+cudaError_t launch_exp_dresp(const ExpCall &c, cudaStream_t s) {
+    // entries without an expert get 0
+    cudaError_t e = cudaMemsetAsync(c.dresp, 0, (size_t)c.s.P * sizeof(float), s);
+    if (e != cudaSuccess) return e;
+    switch (c.s.dt) {
+        case GMM_F32: dresp_t<float>(c, s); break;
+        case GMM_BF16: dresp_t<__nv_bfloat16>(c, s); break;
+        default: dresp_t<__half>(c, s);
+    }
+    note_launches(1);
+    return cudaGetLastError();
+}
+
+// ------------------------------------------------------ bias gradients
+// Column sums over each expert's rows: 32 columns x 8 row lanes per block.
+// GATHER: rows are dy's, weighted by resp; otherwise rows of da.
+template <typename T, typename E, bool GATHER>
+__global__ void __launch_bounds__(256)
+exp_colsum_kernel(ExpRoute rt, const E *__restrict__ rows, const float *__restrict__ resp,
+                  int width, T *__restrict__ out) {
+    __shared__ float sh[8][33];
+    const int lane = threadIdx.x & 31, ty = threadIdx.x >> 5;
+    const int e = blockIdx.y, col = blockIdx.x * 32 + lane;
+    const int64_t beg = rt.ids ? rt.seg[e] : 0, end = rt.ids ? beg + rt.cnt[e] : rt.N;
+    float acc = 0.f;
+    if (col < width)
+        for (int64_t row = beg + ty; row < end; row += 8) {
+            if (GATHER) {
+                const int64_t p = rt.pair(row);
+                acc = fmaf(resp ? resp[p] : 1.f, to_float(rows[rt.token(p) * width + col]), acc);
+            } else {
+                acc += to_float(rows[row * width + col]);
+            }
+        }
+    sh[ty][lane] = acc;
+    __syncthreads();
+    if (ty == 0 && col < width) {
+        float t = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t += sh[i][lane];
+        out[(size_t)e * width + col] = from_float<T>(t);
+    }
+}
+
+template <typename T> static void bias_t(const ExpCall &c, cudaStream_t s) {
+    if (c.db1) {
+        const int w = c.s.first();
+        const dim3 grid((w + 31) / 32, c.s.K);
+        if (c.esize == 4)
+            exp_colsum_kernel<T, float, false><<<grid, 256, 0, s>>>(c.rt, (const float *)c.da,
+                                                                    nullptr, w, (T *)c.db1);
+        else
+            exp_colsum_kernel<T, T, false><<<grid, 256, 0, s>>>(c.rt, (const T *)c.da, nullptr, w,
+                                                                (T *)c.db1);
+        note_launches(1);
+    }
+    if (c.db2) {
+        const dim3 grid((c.s.o + 31) / 32, c.s.K);
+        exp_colsum_kernel<T, T, true><<<grid, 256, 0, s>>>(c.rt, (const T *)c.dy, c.resp, c.s.o,
+                                                           (T *)c.db2);
+        note_launches(1);
+    }
+}
+
+cudaError_t launch_exp_bias_grads(const ExpCall &c, cudaStream_t s) {
+    switch (c.s.dt) {
+        case GMM_F32: bias_t<float>(c, s); break;
+        case GMM_BF16: bias_t<__nv_bfloat16>(c, s); break;
+        default: bias_t<__half>(c, s);
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace gmmb
