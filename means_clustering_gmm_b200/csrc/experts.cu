@@ -41,7 +41,12 @@ ExpShape make_shape(const gmm_expert_shape *s) {
     return p;
 }
 
-int path_of(const ExpShape &, bool, uint32_t) { return 0; }
+int path_of(const ExpShape &p, bool, uint32_t flags) {
+    if (flags & GMM_FLAG_FORCE_SIMT) return 0;
+    // tensor maps want rows of whole 16-byte units
+    if (p.dt == GMM_F32 || p.d % 8 || p.h % 8 || p.o % 8) return 0;
+    return 2;
+}
 
 struct Layout {
     size_t cnt, seg, tile_expert, ntiles, row_pair, hist, hid, da, slots, rpart, total;
@@ -58,7 +63,7 @@ Layout layout_of(const ExpShape &p, bool backward, int path) {
     L.max_rows = (int64_t)L.max_tiles * kExpTile;
     L.esize = path == 0 ? 4 : 2;
     const int width = p.mlp ? p.h : p.o;
-    L.nrpart = (width + 63) / 64;
+    L.nrpart = path == 0 ? (width + 63) / 64 : exp_tc_resp_parts(p);
     size_t o = kAlign;   // error word
     auto take = [&](size_t &off, size_t bytes) {
         off = o;
@@ -161,7 +166,8 @@ gmm_status forward(const gmm_expert_shape *shape, bool mlp, const void *X, const
     c.resp = resp;
     c.y = Y;
     if (launch_exp_route(c, s) != cudaSuccess) return GMM_ERR_CUDA;
-    if (launch_exp_simt(c, false, s) != cudaSuccess) return GMM_ERR_CUDA;
+    if ((path == 0 ? launch_exp_simt(c, false, s) : launch_exp_tc(c, false, s)) != cudaSuccess)
+        return GMM_ERR_CUDA;
     if (!p.direct() && launch_exp_combine(c, false, s) != cudaSuccess) return GMM_ERR_CUDA;
     return GMM_OK;
 }
@@ -213,7 +219,8 @@ gmm_status backward(const gmm_expert_shape *shape, bool mlp, const void *dY, con
     c.db2 = db2;
     c.dresp = dresp;
     if (launch_exp_route(c, s) != cudaSuccess) return GMM_ERR_CUDA;
-    if (launch_exp_simt(c, true, s) != cudaSuccess) return GMM_ERR_CUDA;
+    if ((path == 0 ? launch_exp_simt(c, true, s) : launch_exp_tc(c, true, s)) != cudaSuccess)
+        return GMM_ERR_CUDA;
     if (!p.direct() && launch_exp_combine(c, true, s) != cudaSuccess) return GMM_ERR_CUDA;
     if (launch_exp_bias_grads(c, s) != cudaSuccess) return GMM_ERR_CUDA;
     if (dresp && launch_exp_dresp(c, s) != cudaSuccess) return GMM_ERR_CUDA;

@@ -126,5 +126,8 @@ cudaError_t launch_exp_dresp(const ExpCall &c, cudaStream_t s);
 cudaError_t launch_exp_bias_grads(const ExpCall &c, cudaStream_t s);
 // experts_simt.cu: the products on CUDA cores
 cudaError_t launch_exp_simt(const ExpCall &c, bool backward, cudaStream_t s);
+// experts_tc.cu: on the tensor cores (16-bit types, widths multiples of 8)
+cudaError_t launch_exp_tc(const ExpCall &c, bool backward, cudaStream_t s);
+int exp_tc_resp_parts(const ExpShape &s);
 
 }  // namespace gmmb

@@ -43,6 +43,9 @@ def test_sizes_and_flags():
     assert size(shape(h=64)) > size(shape())
     assert size(shape(), 0, 64) == 0
     assert size(shape(r=0, K=1)) > 0
+    # 16-bit operands for the tensor cores, fp32 ones for the CUDA cores
+    big = shape(N=10000, h=1024, d=512, o=512)
+    assert size(big, 1) < size(big, 1, _lib.GMM_FLAG_FORCE_SIMT)
     # nothing of size N x K x width: rows grow with the pairs
     assert size(shape(N=100000, h=64, K=64), 1) < 2 * size(shape(N=100000, h=64, K=4), 1)
     assert _lib.load().gmm_expert_workspace_size(None, 0, 0) == 0
@@ -94,6 +97,7 @@ def test_backward_refusals():
     assert call(ids=None) == E
     assert call(wsb=need - 1) == E
     assert call(ws=A + 128) == E
+    assert call(fl=2) == E                        # the CUDA-core form needs more workspace
     assert call(s=shape()) == E
     assert call(dX=A + 4096) == E                 # X itself
     fwd = size(shape(h=64), 0)
