@@ -49,7 +49,7 @@ int path_of(const ExpShape &p, bool, uint32_t flags) {
 }
 
 struct Layout {
-    size_t cnt, seg, tile_expert, ntiles, row_pair, hist, hid, da, slots, rpart, total;
+    size_t cnt, seg, tile_expert, ntiles, row_pair, hist, hid, da, xrows, dyrows, slots, rpart, total;
     int64_t max_rows;
     int max_tiles, nrpart;
     size_t esize;
@@ -79,6 +79,9 @@ Layout layout_of(const ExpShape &p, bool backward, int path) {
     take(L.hist, chunks * KK * 4);
     take(L.hid, p.mlp ? (size_t)L.max_rows * p.h * L.esize : 0);
     take(L.da, backward ? (size_t)L.max_rows * p.first() * L.esize : 0);
+    const bool sorted = path == 2 && !p.dense;
+    take(L.xrows, sorted ? (size_t)L.max_rows * p.d * 2 : 0);
+    take(L.dyrows, sorted && backward ? (size_t)L.max_rows * p.o * 2 : 0);
     const int wide = !backward ? p.o : (p.d > p.o ? p.d : p.o);
     take(L.slots, p.direct() ? 0 : (size_t)p.P * wide * 4);
     take(L.rpart, backward ? (size_t)L.max_rows * L.nrpart * 4 : 0);
@@ -105,6 +108,9 @@ ExpCall make_call(const ExpShape &p, const Layout &L, void *ws, const int32_t *i
     c.rt.max_tiles = L.max_tiles;
     c.hid = b + L.hid;
     c.da = b + L.da;
+    c.xrows = b + L.xrows;
+    c.dyrows = b + L.dyrows;
+    c.point_rows = p.dense ? p.N : L.max_rows;
     c.slots = (float *)(b + L.slots);
     c.rpart = (float *)(b + L.rpart);
     c.max_rows = L.max_rows;
@@ -134,6 +140,19 @@ struct Checks {
         ok = ok && ws && aligned(ws, kAlign) && have >= need;
     }
 };
+
+// The products of one call, after its routing.
+cudaError_t products(ExpCall &c, int path, bool backward, cudaStream_t s) {
+    if (path == 0) return launch_exp_simt(c, backward, s);
+    if (c.s.dense) {
+        c.xrows = const_cast<void *>(c.x);
+        c.dyrows = const_cast<void *>(c.dy);
+    } else {
+        const cudaError_t e = launch_exp_gather(c, backward, s);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_exp_tc(c, backward, s);
+}
 
 gmm_status forward(const gmm_expert_shape *shape, bool mlp, const void *X, const int32_t *ids,
                    const float *resp, const void *W1, const void *b1, const void *W2,
@@ -166,8 +185,7 @@ gmm_status forward(const gmm_expert_shape *shape, bool mlp, const void *X, const
     c.resp = resp;
     c.y = Y;
     if (launch_exp_route(c, s) != cudaSuccess) return GMM_ERR_CUDA;
-    if ((path == 0 ? launch_exp_simt(c, false, s) : launch_exp_tc(c, false, s)) != cudaSuccess)
-        return GMM_ERR_CUDA;
+    if (products(c, path, false, s) != cudaSuccess) return GMM_ERR_CUDA;
     if (!p.direct() && launch_exp_combine(c, false, s) != cudaSuccess) return GMM_ERR_CUDA;
     return GMM_OK;
 }
@@ -219,8 +237,7 @@ gmm_status backward(const gmm_expert_shape *shape, bool mlp, const void *dY, con
     c.db2 = db2;
     c.dresp = dresp;
     if (launch_exp_route(c, s) != cudaSuccess) return GMM_ERR_CUDA;
-    if ((path == 0 ? launch_exp_simt(c, true, s) : launch_exp_tc(c, true, s)) != cudaSuccess)
-        return GMM_ERR_CUDA;
+    if (products(c, path, true, s) != cudaSuccess) return GMM_ERR_CUDA;
     if (!p.direct() && launch_exp_combine(c, true, s) != cudaSuccess) return GMM_ERR_CUDA;
     if (launch_exp_bias_grads(c, s) != cudaSuccess) return GMM_ERR_CUDA;
     if (dresp && launch_exp_dresp(c, s) != cudaSuccess) return GMM_ERR_CUDA;

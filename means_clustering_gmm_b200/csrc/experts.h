@@ -73,6 +73,10 @@ struct ExpCall {
     // (backward), of the first layer's pre-activation gradient, per-pair
     // results before the sum over entries, and partial sums of dresp
     void *hid, *da;
+    // rows of X and dY sorted by expert, zeros past each segment (tensor
+    // cores; the arrays themselves in the dense form), and how many
+    void *xrows, *dyrows;
+    int64_t point_rows;
     float *slots, *rpart;
     int64_t max_rows;
     int nrpart;         // partial sums of dresp per row
@@ -119,6 +123,8 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(f
 
 // experts_route.cu
 cudaError_t launch_exp_route(const ExpCall &c, cudaStream_t s);
+// the rows of X (and dY) sorted by expert (16-bit types, 16-byte rows)
+cudaError_t launch_exp_gather(const ExpCall &c, bool backward, cudaStream_t s);
 // y_n = sum_i g_ni slots_ni (+ residual_n); dx_n = sum_i slots_ni
 cudaError_t launch_exp_combine(const ExpCall &c, bool backward, cudaStream_t s);
 // dresp from its partial sums (and <dy, b2>); column sums of da and g dy

@@ -169,37 +169,126 @@ cudaError_t launch_exp_route(const ExpCall &c, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-// ------------------------------------------------------------- combine
-// One thread per output element (columns fastest): reads r rows of slots and
-// writes one result; bound by HBM.
-template <typename T, bool BWD>
+// -------------------------------------------------------------- gather
+// One warp per row of a segment's tiles: a copy of its point's row, zeros
+// past the segment (the weight gradients contract over whole tiles).  Bound
+// by HBM.
 __global__ void __launch_bounds__(256)
-exp_combine_kernel(ExpRoute rt, const float *__restrict__ slots, const float *__restrict__ resp,
-                   const T *res, T *out, int width) {
-    const int col = blockIdx.x * 256 + threadIdx.x;
-    if (col >= width) return;
-    for (int64_t n = blockIdx.y; n < rt.N; n += gridDim.y) {
-        float acc = 0.f;
-        for (int i = 0; i < rt.r; ++i) {
-            const int64_t p = n * rt.r + i;
-            if (!rt.used(p)) continue;
-            const float v = slots[p * width + col];
-            acc = BWD ? acc + v : fmaf(resp ? resp[p] : 1.f, v, acc);
+exp_gather_kernel(ExpRoute rt, const uint4 *__restrict__ x, uint4 *__restrict__ xrows, int xu,
+                  const uint4 *__restrict__ dy, uint4 *__restrict__ dyrows, int dyu) {
+    const int lane = threadIdx.x & 31;
+    const int64_t rows = (int64_t)rt.tiles() * kExpTile;
+    const uint4 *src = blockIdx.y ? dy : x;
+    uint4 *dst = blockIdx.y ? dyrows : xrows;
+    const int u = blockIdx.y ? dyu : xu;
+    for (int64_t row = blockIdx.x * 8 + (threadIdx.x >> 5); row < rows; row += gridDim.x * 8) {
+        const auto t = rt.tile((int)(row / kExpTile));
+        if (t.expert >= rt.K) continue;
+        uint4 *o = dst + row * u;
+        if (row < t.seg_end) {
+            const uint4 *p = src + rt.token(rt.pair(row)) * u;
+            int i = lane;
+            for (; i + 96 < u; i += 128) {
+                const uint4 a = p[i], b = p[i + 32], c = p[i + 64], d = p[i + 96];
+                o[i] = a;
+                o[i + 32] = b;
+                o[i + 64] = c;
+                o[i + 96] = d;
+            }
+            for (; i < u; i += 32) o[i] = p[i];
+        } else {
+            for (int i = lane; i < u; i += 32) o[i] = make_uint4(0u, 0u, 0u, 0u);
         }
-        if (!BWD && res) acc += to_float(res[n * width + col]);
-        out[n * width + col] = from_float<T>(acc);
     }
 }
 
+cudaError_t launch_exp_gather(const ExpCall &c, bool backward, cudaStream_t s) {
+    const int64_t want = (c.max_rows + 7) / 8;
+    const dim3 grid((unsigned)(want < 148 * 8 ? want : 148 * 8), backward ? 2 : 1);
+    exp_gather_kernel<<<grid, 256, 0, s>>>(c.rt, (const uint4 *)c.x, (uint4 *)c.xrows, c.s.d / 8,
+                                           (const uint4 *)c.dy, (uint4 *)c.dyrows, c.s.o / 8);
+    note_launches(1);
+    return cudaGetLastError();
+}
+
+// ------------------------------------------------------------- combine
+// The sum of a point's entries: reads r rows of slots and writes one result;
+// bound by HBM.  A thread takes V columns (8: float4 reads, one 16- or
+// 32-byte write; 1: odd widths or a residual that is not 16-byte aligned).
+template <typename T, bool BWD, int V>
+__global__ void __launch_bounds__(256)
+exp_combine_kernel(ExpRoute rt, const float *__restrict__ slots, const float *__restrict__ resp,
+                   const T *res, T *out, int width) {
+    const int units = width / V;
+    const int64_t total = rt.N * units;
+    for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < total;
+         i += (int64_t)gridDim.x * 256) {
+        const int64_t n = i / units;
+        const int col = (int)(i - n * units) * V;
+        float acc[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[v] = 0.f;
+        for (int e = 0; e < rt.r; ++e) {
+            const int64_t p = n * rt.r + e;
+            if (!rt.used(p)) continue;
+            const float g = BWD || !resp ? 1.f : resp[p];
+            const float *s = slots + p * width + col;
+            float x[V];
+            if constexpr (V == 8) {
+                const float4 lo = __ldcs(reinterpret_cast<const float4 *>(s));
+                const float4 hi = __ldcs(reinterpret_cast<const float4 *>(s) + 1);
+                x[0] = lo.x; x[1] = lo.y; x[2] = lo.z; x[3] = lo.w;
+                x[4] = hi.x; x[5] = hi.y; x[6] = hi.z; x[7] = hi.w;
+            } else {
+                x[0] = *s;
+            }
+#pragma unroll
+            for (int v = 0; v < V; ++v) acc[v] = BWD ? acc[v] + x[v] : fmaf(g, x[v], acc[v]);
+        }
+        __align__(16) T o[V];
+        if (!BWD && res) {
+            __align__(16) T b[V];
+            if constexpr (V == 8) {
+                const uint4 *w = reinterpret_cast<const uint4 *>(res + n * width + col);
+                uint4 *d = reinterpret_cast<uint4 *>(b);
+#pragma unroll
+                for (int k = 0; k < (int)(V * sizeof(T) / 16); ++k) d[k] = w[k];
+            } else {
+                b[0] = res[n * width + col];
+            }
+#pragma unroll
+            for (int v = 0; v < V; ++v) acc[v] += to_float(b[v]);
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) o[v] = from_float<T>(acc[v]);
+        if constexpr (V == 8) {
+            uint4 *w = reinterpret_cast<uint4 *>(out + n * width + col);
+            const uint4 *d = reinterpret_cast<const uint4 *>(o);
+#pragma unroll
+            for (int k = 0; k < (int)(V * sizeof(T) / 16); ++k) w[k] = d[k];
+        } else {
+            out[n * width + col] = o[0];
+        }
+    }
+}
+
+template <typename T, bool BWD, int V> static void combine_v(const ExpCall &c, cudaStream_t s) {
+    const int width = BWD ? c.s.d : c.s.o;
+    const int64_t want = (c.s.N * (width / V) + 255) / 256;
+    const unsigned grid = (unsigned)(want < 148 * 16 ? want : 148 * 16);
+    exp_combine_kernel<T, BWD, V><<<grid, 256, 0, s>>>(
+        c.rt, c.slots, BWD ? nullptr : c.resp, BWD ? nullptr : (const T *)c.res,
+        (T *)(BWD ? c.dx : c.y), width);
+}
+
 template <typename T> static void combine_t(const ExpCall &c, bool backward, cudaStream_t s) {
-    const int width = backward ? c.s.d : c.s.o;
-    const dim3 grid((width + 255) / 256, (unsigned)(c.s.N < 32768 ? c.s.N : 32768));
-    if (backward)
-        exp_combine_kernel<T, true><<<grid, 256, 0, s>>>(c.rt, c.slots, nullptr, nullptr,
-                                                         (T *)c.dx, width);
-    else
-        exp_combine_kernel<T, false><<<grid, 256, 0, s>>>(c.rt, c.slots, c.resp, (const T *)c.res,
-                                                          (T *)c.y, width);
+    if (backward) {
+        if (c.s.d % 8 == 0) combine_v<T, true, 8>(c, s);
+        else combine_v<T, true, 1>(c, s);
+    } else {
+        if (c.s.o % 8 == 0 && ((uintptr_t)c.res & 15) == 0) combine_v<T, false, 8>(c, s);
+        else combine_v<T, false, 1>(c, s);
+    }
 }
 
 cudaError_t launch_exp_combine(const ExpCall &c, bool backward, cudaStream_t s) {

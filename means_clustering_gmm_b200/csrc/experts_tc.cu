@@ -2,12 +2,16 @@
 // multiples of 8): one persistent kernel template, one CTA per SM, for every
 // product of both directions.
 //
-//   warp 0       TMA producer.  Rows that belong to points are fetched by
-//                index (tile::gather4, four rows an instruction, each lane
-//                its own four), so no permuted copy of X or dY is made;
-//                weights and workspace rows come as plain boxes.  Rows,
-//                columns and contraction indices past an edge arrive as
-//                zeros from the tensor map.
+//   warp 0       TMA producer.  Rows of X and dY come from copies sorted by
+//                expert (the arrays themselves in the dense form).  Fetching
+//                them in place by index (tile::gather4) was built first and
+//                bounded every product that used it: a gather of four rows
+//                takes an SM's TMA unit about 40 ns, 1.3 us for a stage whose
+//                products take 0.27 us (8192 points, 2048-4096 gated: 1266 us
+//                against 238 us a half-sized product from boxes), where the
+//                copy costs two passes over the rows.  Rows, columns and
+//                contraction indices past an edge arrive as zeros from the
+//                tensor map.
 //   warp 1       tcgen05.mma, M = 128, N up to 256, fp32 accumulators in
 //                TMEM, two buffers of 256 columns: the epilogue of one tile
 //                runs under the products of the next.
@@ -158,6 +162,7 @@ __global__ void __launch_bounds__(kThreads, 1) exp_tc_kernel(const __grid_consta
     const ExpCall &c = a.c;
     const ExpShape &s = c.s;
     const ExpRoute &rt = c.rt;
+    (void)rt;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         for (int i = 0; i < C::kStages; ++i) {
@@ -187,80 +192,50 @@ __global__ void __launch_bounds__(kThreads, 1) exp_tc_kernel(const __grid_consta
     if (warp == 0) {
         // ================================================ TMA producer
         uint32_t fill = 0;   // stages filled so far
-        bool ok = true;
-        for (int idx = blockIdx.x; idx < total && ok; idx += gridDim.x) {
-            const Job j = job_of<KIND, GATED>(a, idx);
-            // this lane's gathered rows: of the tile (its rows 4 lane ..), or,
-            // for a weight gradient, of the next step (rows 4 (lane % 16) ..)
-            int tok[4];
-            auto tokens = [&](int64_t row) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    int64_t r = row + i;
-                    // past the segment: its last row again (zeros meet it)
-                    if (r >= j.seg_end) r = j.seg_end - 1;
-                    tok[i] = (int)rt.token(rt.pair(r));
-                }
-            };
-            const int steps = j.steps1 + j.steps2;
-            if (steps > 0) tokens(C::kGrad ? j.row0 + 4 * (lane & 15) : j.row0 + 4 * lane);
-            for (int st = 0; st < steps; ++st, ++fill) {
-                const int slot = fill % C::kStages;
-                const uint32_t ph = (fill / C::kStages) & 1;
-                ok = __all_sync(0xffffffffu,
-                                mbar_wait(&bars->empty[slot], ph ^ 1, c.err, abort_flag));
-                if (!ok) break;
-                uint8_t *A = sm + (size_t)slot * C::kStage, *B = A + kBytesA;
-                uint64_t *bar = &bars->full[slot];
-                const bool second = KIND == kDaMlp && st >= j.steps1;
-                if (lane == 0)
+        if (lane == 0) {
+            bool ok = true;
+            for (int idx = blockIdx.x; idx < total && ok; idx += gridDim.x) {
+                const Job j = job_of<KIND, GATED>(a, idx);
+                const int steps = j.steps1 + j.steps2, row = (int)j.row0;
+                for (int st = 0; st < steps; ++st, ++fill) {
+                    const int slot = fill % C::kStages;
+                    ok = mbar_wait(&bars->empty[slot], ((fill / C::kStages) & 1) ^ 1, c.err,
+                                   abort_flag);
+                    if (!ok) break;
+                    uint8_t *A = sm + (size_t)slot * C::kStage, *B = A + kBytesA;
+                    uint64_t *bar = &bars->full[slot];
+                    const bool second = KIND == kDaMlp && st >= j.steps1;
                     mbar_arrive_expect_tx(
                         bar, kBytesA + (second ? C::N2 * kStepK * 2 : C::N1 * kStepK * 2));
-                __syncwarp();
-                const int k = (second ? st - j.steps1 : st) * kStepK;
-                const int4 rows = make_int4(tok[0], tok[1], tok[2], tok[3]);
-                if constexpr (C::kGrad) {
-                    const int row = (int)j.row0 + k, grp = lane & 15, hi = lane >> 4;
-                    if constexpr (KIND == kDw2) {
-                        tma_gather4(A + hi * kBlk + grp * 512, &a.a, j.m0 + hi * 64, rows, bar);
-                        if (lane < 4)
-                            tma_g2s_2d(B + lane * kBlk, &a.b, j.col0 + lane * 64, row, bar);
+                    const int k = (second ? st - j.steps1 : st) * kStepK;
+                    if constexpr (C::kGrad) {
+#pragma unroll
+                        for (int i = 0; i < kRowsA / 64; ++i)
+                            tma_g2s_2d(A + i * kBlk, &a.a, j.m0 + i * 64, row + k, bar);
+#pragma unroll
+                        for (int i = 0; i < C::NB / 64; ++i)
+                            tma_g2s_2d(B + i * kBlk, &a.b, j.col0 + i * 64, row + k, bar);
                     } else {
-                        if (lane < 2)
-                            tma_g2s_2d(A + lane * kBlk, &a.a, j.m0 + lane * 64, row, bar);
-                        tma_gather4(B + hi * kBlk + grp * 512, &a.b, j.col0 + hi * 64, rows, bar);
-                        tma_gather4(B + (hi + 2) * kBlk + grp * 512, &a.b,
-                                    j.col0 + (hi + 2) * 64, rows, bar);
-                    }
-                    if (st + 1 < steps) tokens(j.row0 + k + kStepK + 4 * grp);
-                } else {
-                    if constexpr (KIND == kSecond || KIND == kDx) {
-                        if (lane == 0) tma_g2s_2d(A, &a.a, k, (int)j.row0, bar);
-                    } else {
-                        tma_gather4(A + lane * 512, second ? &a.a2 : &a.a, k, rows, bar);
-                    }
-                    if constexpr (KIND == kDx) {
-                        if (lane < 4)
-                            tma_g2s_3d(B + lane * kBlk, &a.b, j.col0 + lane * 64, k, j.expert, bar);
-                    } else if (second) {
-                        if (lane < C::N2 / 64)
-                            tma_g2s_3d(B + lane * kBlk, &a.b2, j.col0 + lane * 64, k, j.expert,
-                                       bar);
-                    } else if constexpr (GATED) {
-                        // the tile's gate rows, then its up rows
-                        if (lane < 2)
-                            tma_g2s_3d(B + lane * (C::kBytesB / 2), &a.b, k,
-                                       j.col0 + lane * s.h, j.expert, bar);
-                    } else {
-                        if (lane == 0) tma_g2s_3d(B, &a.b, k, j.col0, j.expert, bar);
+                        tma_g2s_2d(A, second ? &a.a2 : &a.a, k, row, bar);
+                        if (KIND == kDx || second) {
+                            constexpr int n = (KIND == kDx ? C::N1 : C::N2) / 64;
+#pragma unroll
+                            for (int i = 0; i < n; ++i)
+                                tma_g2s_3d(B + i * kBlk, second ? &a.b2 : &a.b, j.col0 + i * 64, k,
+                                           j.expert, bar);
+                        } else if constexpr (GATED) {
+                            // the tile's gate rows, then its up rows
+                            tma_g2s_3d(B, &a.b, k, j.col0, j.expert, bar);
+                            tma_g2s_3d(B + C::kBytesB / 2, &a.b, k, j.col0 + s.h, j.expert, bar);
+                        } else {
+                            tma_g2s_3d(B, &a.b, k, j.col0, j.expert, bar);
+                        }
                     }
                 }
             }
         }
-        __syncwarp();
         // no copy in flight at teardown
-        const uint32_t first = fill > (uint32_t)C::kStages ? fill - C::kStages : 0;
-        for (uint32_t f = first; f < fill; ++f)
+        for (uint32_t f = fill > (uint32_t)C::kStages ? fill - C::kStages : 0; f < fill; ++f)
             mbar_wait_drain(&bars->full[f % C::kStages], (f / C::kStages) & 1, c.err);
     } else if (warp == 1) {
         // ================================================ MMA issuer
@@ -528,10 +503,10 @@ cudaError_t launch_kind(const ExpCall &c, cudaStream_t st) {
         case kDaLin:
         case kDaMlp:
             width = s.mlp ? s.h : s.o;
-            maps.make(&a.a, c.x, s.d, s.N, 0, 1);
+            maps.make(&a.a, c.xrows, s.d, c.point_rows, 0, kRowsA);
             maps.make(&a.b, c.w1, s.d, s.first(), s.K, GATED ? C::N1 / 2 : C::N1);
             if (KIND == kDaMlp) {
-                maps.make(&a.a2, c.dy, s.o, s.N, 0, 1);
+                maps.make(&a.a2, c.dyrows, s.o, c.point_rows, 0, kRowsA);
                 maps.make(&a.b2, c.w2, s.h, s.o, s.K, kStepK);
             }
             break;
@@ -549,12 +524,12 @@ cudaError_t launch_kind(const ExpCall &c, cudaStream_t st) {
             width = s.d;
             mrows = s.first();
             maps.make(&a.a, c.da, s.first(), c.max_rows, 0, kStepK);
-            maps.make(&a.b, c.x, s.d, s.N, 0, 1);
+            maps.make(&a.b, c.xrows, s.d, c.point_rows, 0, kStepK);
             break;
         case kDw2:
             width = s.h;
             mrows = s.o;
-            maps.make(&a.a, c.dy, s.o, s.N, 0, 1);
+            maps.make(&a.a, c.dyrows, s.o, c.point_rows, 0, kStepK);
             maps.make(&a.b, c.hid, s.h, c.max_rows, 0, kStepK);
             break;
     }

@@ -136,16 +136,6 @@ __device__ __forceinline__ void tma_g2s_3d(void *dst_smem, const void *map, int 
         ::"r"(smem_u32(dst_smem)), "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
         : "memory");
 }
-// Four rows of a 2-D tensor map whose box is one row high.
-__device__ __forceinline__ void tma_gather4(void *dst_smem, const void *map, int x, int4 rows,
-                                            uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];"
-        ::"r"(smem_u32(dst_smem)), "l"(map), "r"(x), "r"(rows.x), "r"(rows.y), "r"(rows.z),
-        "r"(rows.w), "r"(smem_u32(bar))
-        : "memory");
-}
 __device__ __forceinline__ void prefetch_tensormap(const void *map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
