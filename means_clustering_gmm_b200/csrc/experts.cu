@@ -49,7 +49,7 @@ int path_of(const ExpShape &p, bool, uint32_t flags) {
 }
 
 struct Layout {
-    size_t cnt, seg, tile_expert, ntiles, row_pair, hist, hid, da, xrows, dyrows, slots, rpart, total;
+    size_t cnt, seg, tile_expert, pair_at, ntiles, row_pair, hist, hid, da, xrows, dyrows, slots, rpart, total;
     int64_t max_rows;
     int max_tiles, nrpart;
     size_t esize;
@@ -74,7 +74,8 @@ Layout layout_of(const ExpShape &p, bool backward, int path) {
     take(L.cnt, p.dense ? 0 : KK * 4);
     take(L.seg, p.dense ? 0 : (KK + 1) * 4);
     take(L.tile_expert, p.dense ? 0 : (size_t)L.max_tiles * 4);
-    take(L.ntiles, 4);
+    take(L.pair_at, p.dense ? 0 : (size_t)L.max_tiles * 8);
+    take(L.ntiles, 8);
     take(L.row_pair, p.dense ? 0 : (size_t)L.max_rows * 4);
     take(L.hist, chunks * KK * 4);
     take(L.hid, p.mlp ? (size_t)L.max_rows * p.h * L.esize : 0);
@@ -97,6 +98,7 @@ ExpCall make_call(const ExpShape &p, const Layout &L, void *ws, const int32_t *i
     c.rt.cnt = (int *)(b + L.cnt);
     c.rt.seg = (int *)(b + L.seg);
     c.rt.tile_expert = (int *)(b + L.tile_expert);
+    c.rt.pair_at = (int2 *)(b + L.pair_at);
     c.rt.ntiles = (int *)(b + L.ntiles);
     c.rt.row_pair = (int *)(b + L.row_pair);
     c.rt.hist = (int *)(b + L.hist);
@@ -106,6 +108,7 @@ ExpCall make_call(const ExpShape &p, const Layout &L, void *ws, const int32_t *i
     c.rt.K = p.K;
     c.rt.r = p.r ? p.r : 1;
     c.rt.max_tiles = L.max_tiles;
+    c.rt.tile_rows = p.P >= kExpPairRows * p.K ? 2 * kExpTile : kExpTile;
     c.hid = b + L.hid;
     c.da = b + L.da;
     c.xrows = b + L.xrows;

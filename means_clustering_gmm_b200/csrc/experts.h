@@ -24,30 +24,48 @@ struct ExpShape {
     __host__ __device__ int first() const { return mlp ? gh : o; }   // width of the first product
 };
 
-// Device view of the routing.  Tile t holds rows [128 t, 128 t + valid).
+// Rows per expert from which a product's tile is two 128-row tiles of one
+// segment on a pair of CTAs.
+constexpr int64_t kExpPairRows = 384;
+
+// Device view of the routing.  Tile t of 128 rows holds rows 128 t .. of its
+// expert; a tile of 256 rows is two of those, the second possibly past the
+// segment.
 struct ExpRoute {
     int *cnt;           // [K + 1] pairs of each expert; [K]: points without any (direct only)
     int *seg;           // [K + 2] first row of each segment
-    int *tile_expert;   // [max tiles]
-    int *ntiles;        // [1]
+    int *tile_expert;   // [max_tiles] expert of each 128-row tile
+    int2 *pair_at;      // [max_tiles] expert and first row of each 256-row tile
+    int *ntiles;        // [2] 128-row and 256-row tiles
     int *row_pair;      // [max rows] pair of each valid row
     int *hist;          // [chunks x (K + 1)]
     const int32_t *ids; // NULL: dense
     int64_t N, P;
     int K, r;
-    int max_tiles;
+    int max_tiles;      // of 128 rows
+    int tile_rows;      // of the products' tiles
 
     struct Tile { int expert, valid; int64_t row0, seg_end; };
-    __device__ __forceinline__ int tiles() const {
-        return ids ? *ntiles : (int)((N + kExpTile - 1) / kExpTile);
+    __device__ __forceinline__ int tiles(int rows = kExpTile) const {
+        return ids ? ntiles[rows == kExpTile ? 0 : 1] : (int)((N + rows - 1) / rows);
     }
-    __device__ __forceinline__ Tile tile(int t) const {
+    __device__ __forceinline__ Tile tile(int t, int rows = kExpTile) const {
         Tile x;
-        x.row0 = (int64_t)t * kExpTile;
-        x.expert = ids ? tile_expert[t] : 0;
-        x.seg_end = ids ? (int64_t)seg[x.expert] + cnt[x.expert] : N;
+        x.expert = 0;
+        x.row0 = (int64_t)t * rows;
+        x.seg_end = N;
+        if (ids) {
+            if (rows == kExpTile) {
+                x.expert = tile_expert[t];
+            } else {
+                const int2 at = pair_at[t];
+                x.expert = at.x;
+                x.row0 = at.y;
+            }
+            x.seg_end = (int64_t)seg[x.expert] + cnt[x.expert];
+        }
         const int64_t v = x.seg_end - x.row0;
-        x.valid = v < kExpTile ? (int)v : kExpTile;
+        x.valid = v < rows ? (int)v : rows;
         return x;
     }
     __device__ __forceinline__ int64_t pair(int64_t row) const {
@@ -105,6 +123,33 @@ template <int ACT> __device__ __forceinline__ float act_of(float z) {
     float f, df;
     act_both<ACT>(z, f, df);
     return f;
+}
+
+// The same to fp32 precision of z rather than of f, for results that are
+// rounded to 16 bits: hardware exponential and reciprocal (2^-21), and for
+// gelu erfc by Abramowitz and Stegun 7.1.26 (absolute error 1.5e-7), whose
+// exponential is the density's too.  About 20 instructions where erfcf and
+// expf take about 55; the epilogue of a 4096 x 1024 x 4096 gelu map is bound
+// by them.
+template <int ACT> __device__ __forceinline__ void act_fast(float z, float &f, float &df) {
+    if (ACT == GMM_ACT_GELU) {
+        const float t = __fdividef(1.f, fmaf(0.3275911f * 0.70710678f, fabsf(z), 1.f));
+        float p = fmaf(1.061405429f, t, -1.453152027f);
+        p = fmaf(p, t, 1.421413741f);
+        p = fmaf(p, t, -0.284496736f);
+        p = fmaf(p, t, 0.254829592f);
+        const float e = __expf(-0.5f * z * z);
+        const float tail = 0.5f * p * t * e;
+        const float cdf = z >= 0.f ? 1.f - tail : tail;
+        f = z * cdf;
+        df = fmaf(z, 0.39894228f * e, cdf);
+    } else if (ACT == GMM_ACT_SILU) {
+        const float p = __fdividef(1.f, 1.f + __expf(-z));
+        f = z * p;
+        df = p * fmaf(z, 1.f - p, 1.f);
+    } else {
+        act_both<ACT>(z, f, df);
+    }
 }
 
 // An ordinary load: the compiler keeps it behind the test that guards it,

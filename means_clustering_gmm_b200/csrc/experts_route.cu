@@ -63,59 +63,153 @@ exp_scan_kernel(ExpRoute rt, int64_t nch) {
     if (lane == 0) rt.cnt[e] = e < rt.K || rt.r <= 1 ? total : 0;
 }
 
-// One block: segment starts (whole tiles) and the expert of every tile.
-__global__ void __launch_bounds__(1024)
-exp_tiles_kernel(ExpRoute rt) {
-    extern __shared__ int sh[];   // [KK + 1] first tile of each segment
-    __shared__ int wsum[32];
+// One block of 1024: segment starts (whole tiles) and the tables of 128-row
+// and 256-row tiles, from the counts.  sh: [2 x (KK + 1)] ints.
+__device__ __forceinline__ void make_tiles(const ExpRoute &rt, const int *cnt, int *sh) {
+    __shared__ int wsum[2][32];
     const int KK = rt.K + 1, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int *first1 = sh, *first2 = sh + KK + 1;   // first tile of each segment
     const int per = (KK + 1023) / 1024;
-    int mine = 0;
+    int mine1 = 0, mine2 = 0;
     for (int i = 0; i < per; ++i) {
         const int e = tid * per + i;
-        if (e < KK) mine += (rt.cnt[e] + kExpTile - 1) / kExpTile;
+        if (e < KK) {
+            mine1 += (cnt[e] + kExpTile - 1) / kExpTile;
+            mine2 += (cnt[e] + 2 * kExpTile - 1) / (2 * kExpTile);
+        }
     }
-    int x = mine;
+    int x1 = mine1, x2 = mine2;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
+        const int y1 = __shfl_up_sync(0xffffffffu, x1, o);
+        const int y2 = __shfl_up_sync(0xffffffffu, x2, o);
+        if (lane >= o) {
+            x1 += y1;
+            x2 += y2;
+        }
     }
-    if (lane == 31) wsum[warp] = x;
+    if (lane == 31) {
+        wsum[0][warp] = x1;
+        wsum[1][warp] = x2;
+    }
     __syncthreads();
-    if (warp == 0) {
-        int w = wsum[lane];
+    if (warp < 2) {
+        int w = wsum[warp][lane];
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int y = __shfl_up_sync(0xffffffffu, w, o);
             if (lane >= o) w += y;
         }
-        wsum[lane] = w;
+        wsum[warp][lane] = w;
     }
     __syncthreads();
-    int t = x - mine + (warp ? wsum[warp - 1] : 0);
+    int t1 = x1 - mine1 + (warp ? wsum[0][warp - 1] : 0);
+    int t2 = x2 - mine2 + (warp ? wsum[1][warp - 1] : 0);
     for (int i = 0; i < per; ++i) {
         const int e = tid * per + i;
         if (e < KK) {
-            sh[e] = t;
-            rt.seg[e] = t * kExpTile;
-            t += (rt.cnt[e] + kExpTile - 1) / kExpTile;
+            first1[e] = t1;
+            first2[e] = t2;
+            rt.seg[e] = t1 * kExpTile;
+            t1 += (cnt[e] + kExpTile - 1) / kExpTile;
+            t2 += (cnt[e] + 2 * kExpTile - 1) / (2 * kExpTile);
         }
     }
-    const int total = wsum[31];
+    const int total1 = wsum[0][31], total2 = wsum[1][31];
     if (tid == 0) {
-        sh[KK] = total;
-        rt.seg[KK] = total * kExpTile;
-        rt.ntiles[0] = total;
+        rt.seg[KK] = total1 * kExpTile;
+        rt.ntiles[0] = total1;
+        rt.ntiles[1] = total2;
     }
     __syncthreads();
-    for (int i = tid; i < total; i += 1024) {
-        int lo = 0, hi = KK;   // last e with sh[e] <= i
+    for (int i = tid; i < total1 + total2; i += 1024) {
+        const bool two = i >= total1;
+        const int t = two ? i - total1 : i;
+        const int *f = two ? first2 : first1;
+        int lo = 0, hi = KK;   // last e with f[e] <= t
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
-            if (sh[mid] <= i) lo = mid; else hi = mid;
+            if (f[mid] <= t) lo = mid; else hi = mid;
         }
-        rt.tile_expert[i] = lo;
+        if (two) rt.pair_at[t] = make_int2(lo, (first1[lo] + 2 * (t - f[lo])) * kExpTile);
+        else rt.tile_expert[t] = lo;
+    }
+}
+
+__global__ void __launch_bounds__(1024)
+exp_tiles_kernel(ExpRoute rt) {
+    extern __shared__ int sh[];
+    make_tiles(rt, rt.cnt, sh);
+}
+
+// The whole sort in one block, for up to kOneBlockPairs pairs: warp w takes
+// the w-th run of pairs, twice (counts, then places).
+constexpr int kOneBlockPairs = 4096;
+constexpr int kOneBlockKeys = 1024;
+__global__ void __launch_bounds__(1024)
+exp_route_kernel(ExpRoute rt, int *err) {
+    extern __shared__ int sh[];
+    const int KK = rt.K + 1, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int *counts = sh;                    // [32][KK]
+    int *cnt = sh + 32 * KK;             // [KK]
+    int *tiles = cnt + KK;               // [2 x (KK + 1)]
+    int *row = counts + warp * KK;
+    const int P = (int)rt.P;
+    const int run = ((P + 1023) / 1024) * 32;   // pairs of a warp
+    const int beg = warp * run, end = min(beg + run, P);
+    for (int i = tid; i < 32 * KK; i += 1024) counts[i] = 0;
+    __syncthreads();
+    for (int p0 = beg; p0 < end; p0 += 256) {
+        int key[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int p = p0 + u * 32 + lane;
+            key[u] = p < end ? pair_key(rt.ids, p, rt.K, err) : -1;
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const unsigned same = __match_any_sync(0xffffffffu, key[u]);
+            if (key[u] >= 0 && lane == __ffs(same) - 1) row[key[u]] += __popc(same);
+            __syncwarp();
+        }
+    }
+    __syncthreads();
+    for (int e = tid; e < KK; e += 1024) {
+        int t = 0;
+        for (int w = 0; w < 32; ++w) {
+            const int v = counts[w * KK + e];
+            counts[w * KK + e] = t;
+            t += v;
+        }
+        // points without an expert make rows only where the last product
+        // writes the result itself
+        if (e == rt.K && rt.r > 1) t = 0;
+        cnt[e] = t;
+        rt.cnt[e] = t;
+    }
+    __syncthreads();
+    make_tiles(rt, cnt, tiles);
+    __syncthreads();
+    for (int p0 = beg; p0 < end; p0 += 256) {
+        int key[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int p = p0 + u * 32 + lane;
+            key[u] = p < end ? pair_key(rt.ids, p, rt.K, nullptr) : -1;
+            if (key[u] == rt.K && rt.r > 1) key[u] = -1;
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const unsigned same = __match_any_sync(0xffffffffu, key[u]);
+            const int rank = __popc(same & ((1u << lane) - 1));
+            const int base = key[u] >= 0 ? row[key[u]] : 0;
+            __syncwarp();
+            if (key[u] >= 0) {
+                rt.row_pair[tiles[key[u]] * kExpTile + base + rank] = p0 + u * 32 + lane;
+                if (rank == 0) row[key[u]] = base + __popc(same);
+            }
+            __syncwarp();
+        }
     }
 }
 
@@ -150,6 +244,17 @@ cudaError_t launch_exp_route(const ExpCall &c, cudaStream_t s) {
     const ExpRoute &rt = c.rt;
     if (!rt.ids) return cudaSuccess;
     const int KK = rt.K + 1;
+    if (rt.P <= kOneBlockPairs && KK <= kOneBlockKeys) {
+        const int bytes = (35 * KK + 2) * (int)sizeof(int);
+        cudaError_t e = cudaSuccess;
+        if (bytes > 40 * 1024)
+            e = cudaFuncSetAttribute(exp_route_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     bytes);
+        if (e != cudaSuccess) return e;
+        exp_route_kernel<<<1, 1024, bytes, s>>>(rt, c.err);
+        note_launches(1);
+        return cudaGetLastError();
+    }
     const int64_t nch = (rt.P + kChunkPairs - 1) / kChunkPairs;
     const unsigned blocks = (unsigned)((nch + 3) / 4);
     const int smem = 4 * KK * (int)sizeof(int);
@@ -163,7 +268,7 @@ cudaError_t launch_exp_route(const ExpCall &c, cudaStream_t s) {
     }
     exp_hist_kernel<<<blocks, 128, smem, s>>>(rt, c.err);
     exp_scan_kernel<<<(KK + 3) / 4, 128, 0, s>>>(rt, nch);
-    exp_tiles_kernel<<<1, 1024, (KK + 1) * sizeof(int), s>>>(rt);
+    exp_tiles_kernel<<<1, 1024, 2 * (KK + 1) * sizeof(int), s>>>(rt);
     exp_scatter_kernel<<<blocks, 128, smem, s>>>(rt);
     note_launches(4);
     return cudaGetLastError();

@@ -49,22 +49,38 @@ enum Kind {
     kDw2       // dY^T (resp * h)
 };
 
-// Output columns per tile, MMA widths of the (up to two) phases, bytes of a
-// stage's B part and the number of stages.  kDaMlp keeps the pre-activations
-// and q = W2^T dY side by side in one accumulator buffer, so its tile is
-// narrower: 64 columns gated (64 + 64 + 64), 128 otherwise (128 + 128).
-template <int KIND, bool GATED> struct Cfg {
+// Output columns per tile (NB), MMA widths of the (up to two) phases, bytes
+// of a stage and the number of stages.  CG = 2: a pair of CTAs takes 256 rows,
+// each CTA 128 of them and half of B's rows, which halves what a stage brings
+// of B: a 128 x 256 tile moves 48 KB into and 48 KB out of shared memory for
+// 512 clocks of products, a pair's half 32 KB each way, which is what 128
+// bytes a clock can do.
+//
+// kDaMlp keeps the pre-activations and q = W2^T dY side by side: q first
+// (phase 1, two buffers of 128 columns), then the pre-activations (phase 2).
+// Gated, those take the other 256 columns, once: the next tile's phase 1
+// covers the epilogue.  Otherwise they are double-buffered too.
+template <int KIND, bool GATED, int CG> struct Cfg {
     static constexpr bool kGrad = KIND == kDw1 || KIND == kDw2;
-    static constexpr int NB = KIND == kDaMlp ? (GATED ? 64 : 128)
-                              : (KIND == kFirst && GATED) ? 128 : 256;
-    static constexpr int N1 = KIND == kDaMlp ? 128 : 256;
-    static constexpr int N2 = KIND == kDaMlp ? NB : 0;
-    static constexpr int kBytesB = N1 * kStepK * 2;
+    static constexpr bool kTwo = KIND == kDaMlp;
+    static constexpr int NB = kTwo || (KIND == kFirst && GATED) ? 128 : 256;
+    static constexpr int N1 = kTwo ? 128 : 256;
+    static constexpr int N2 = kTwo ? (GATED ? 256 : 128) : 0;
+    static constexpr int kB1 = N1 / CG * kStepK * 2, kB2 = N2 / CG * kStepK * 2;
+    static constexpr int kBytesB = kB1 > kB2 ? kB1 : kB2;
     static constexpr int kStage = kBytesA + kBytesB;
     static constexpr int kStages = 192 * 1024 / kStage;
     static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + 256;
     static constexpr bool kAMn = kGrad;
-    static constexpr bool kBMn = kGrad || KIND == kDx;
+    static constexpr bool kBMn1 = kGrad || KIND == kDx || kTwo;
+    static constexpr int kTileRows = kRowsA * CG;
+    // TMEM columns of tile t's phase 1 and phase 2 accumulators
+    __device__ static constexpr uint32_t col1(uint32_t t) {
+        return (t & 1) * (kTwo && GATED ? 128 : 256);
+    }
+    __device__ static constexpr uint32_t col2(uint32_t t) {
+        return GATED ? 256 : (t & 1) * 256 + 128;
+    }
 };
 
 struct Args {
@@ -78,44 +94,45 @@ struct Bars {
     uint64_t full[8], empty[8], accfull[2], accfree[2], done;
 };
 
-// One tile: which expert, which rows and columns, how many contraction steps.
+// One tile of this CTA: which expert, which rows and columns, how many
+// contraction steps.  valid <= 0: the pair's other CTA holds the segment's
+// last rows, and nothing of this half is stored.
 struct Job {
     int expert, valid, col0, m0, steps1, steps2;
-    int64_t row0, seg_end;
+    int64_t row0;
 };
 
-template <int KIND, bool GATED>
+template <int KIND, bool GATED, int CG>
 __device__ __forceinline__ int total_jobs(const Args &a) {
-    return Cfg<KIND, GATED>::kGrad ? a.c.s.K * a.ntm * a.ntn : a.c.rt.tiles() * a.ntn;
+    return Cfg<KIND, GATED, CG>::kGrad ? a.c.s.K * a.ntm * a.ntn
+                                       : a.c.rt.tiles(CG * kRowsA) * a.ntn;
 }
 
-template <int KIND, bool GATED>
-__device__ __forceinline__ Job job_of(const Args &a, int idx) {
-    using C = Cfg<KIND, GATED>;
+template <int KIND, bool GATED, int CG>
+__device__ __forceinline__ Job job_of(const Args &a, int idx, int rank) {
+    using C = Cfg<KIND, GATED, CG>;
     Job j;
     const ExpShape &s = a.c.s;
     const int t = idx / a.ntn;
     j.col0 = (idx - t * a.ntn) * C::NB;
     if constexpr (C::kGrad) {
         j.expert = t / a.ntm;
-        j.m0 = (t - j.expert * a.ntm) * kRowsA;
+        j.m0 = (t - j.expert * a.ntm) * C::kTileRows + rank * kRowsA;
         const int64_t cnt = a.c.rt.ids ? a.c.rt.cnt[j.expert] : a.c.rt.N;
         j.row0 = a.c.rt.ids ? a.c.rt.seg[j.expert] : 0;
-        j.seg_end = j.row0 + cnt;
         j.valid = kRowsA;
         j.steps1 = (int)((cnt + kStepK - 1) / kStepK);
         j.steps2 = 0;
     } else {
-        const auto x = a.c.rt.tile(t);
+        const auto x = a.c.rt.tile(t, CG * kRowsA);
         j.expert = x.expert;
-        j.valid = x.valid;
-        j.row0 = x.row0;
-        j.seg_end = x.seg_end;
+        j.row0 = x.row0 + rank * kRowsA;
+        j.valid = x.valid - rank * kRowsA < kRowsA ? x.valid - rank * kRowsA : kRowsA;
         j.m0 = 0;
-        const int k1 = KIND == kSecond ? s.h : KIND == kDx ? s.first() : s.d;
+        const int k1 = KIND == kSecond ? s.h : KIND == kDx ? s.first() : C::kTwo ? s.o : s.d;
         const bool none = x.expert >= s.K;
         j.steps1 = none ? 0 : (k1 + kStepK - 1) / kStepK;
-        j.steps2 = KIND == kDaMlp && !none ? (s.o + kStepK - 1) / kStepK : 0;
+        j.steps2 = C::kTwo && !none ? (s.d + kStepK - 1) / kStepK : 0;
     }
     return j;
 }
@@ -148,22 +165,23 @@ __device__ __forceinline__ void store8(T *p, const float (&v)[8]) {
                                                pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7]));
 }
 
-template <typename T, int KIND, int ACT, bool GATED>
+template <typename T, int KIND, int ACT, bool GATED, int CG>
 __global__ void __launch_bounds__(kThreads, 1) exp_tc_kernel(const __grid_constant__ Args a) {
-    using C = Cfg<KIND, GATED>;
+    using C = Cfg<KIND, GATED, CG>;
     extern __shared__ uint8_t raw_smem[];
     uint8_t *sm = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~(uintptr_t)1023);
     Bars *bars = reinterpret_cast<Bars *>(sm + (size_t)C::kStages * C::kStage);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    static_assert(sizeof(Bars) + 8 <= 256, "barrier block");
+    static_assert(sizeof(Bars) + 8 <= 256 && C::kStages <= 8, "barrier block");
 
     const ExpCall &c = a.c;
     const ExpShape &s = c.s;
     const ExpRoute &rt = c.rt;
-    (void)rt;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = CG == 2 ? (int)cluster_ctarank() : 0;
+    const int first = blockIdx.x / CG, stride = gridDim.x / CG;   // this pair's tiles
     if (tid == 0) {
         for (int i = 0; i < C::kStages; ++i) {
             mbar_init(&bars->full[i], 1);
@@ -171,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, 1) exp_tc_kernel(const __grid_consta
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars->accfull[i], 1);
-            mbar_init(&bars->accfree[i], 8);
+            mbar_init(&bars->accfree[i], 8 * CG);
         }
         mbar_init(&bars->done, 1);
         *abort_flag = 0;
@@ -180,22 +198,31 @@ __global__ void __launch_bounds__(kThreads, 1) exp_tc_kernel(const __grid_consta
         prefetch_tensormap(&a.b);
     }
     if (warp == 1) {
-        tmem_alloc(tmem_slot, 512);
-        tmem_relinquish();
+        if constexpr (CG == 2) {
+            tmem_alloc_pair(tmem_slot, 512);
+        } else {
+            tmem_alloc(tmem_slot, 512);
+            tmem_relinquish();
+        }
     }
     tc_fence_before();
-    __syncthreads();
+    if constexpr (CG == 2) cluster_sync_all();
+    else __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const int total = total_jobs<KIND, GATED>(a);
+    const int total = total_jobs<KIND, GATED, CG>(a);
 
     if (warp == 0) {
         // ================================================ TMA producer
+        // Each CTA fetches its own rows of A and its part of B; a pair's
+        // bytes are all counted on the barrier of rank 0, whose one arrival
+        // expects both CTAs' (a slot is refilled only after the products that
+        // read it, so no copy of a later phase can reach an earlier one).
         uint32_t fill = 0;   // stages filled so far
         if (lane == 0) {
             bool ok = true;
-            for (int idx = blockIdx.x; idx < total && ok; idx += gridDim.x) {
-                const Job j = job_of<KIND, GATED>(a, idx);
+            for (int idx = first; idx < total && ok; idx += stride) {
+                const Job j = job_of<KIND, GATED, CG>(a, idx, rank);
                 const int steps = j.steps1 + j.steps2, row = (int)j.row0;
                 for (int st = 0; st < steps; ++st, ++fill) {
                     const int slot = fill % C::kStages;
@@ -203,90 +230,138 @@ __global__ void __launch_bounds__(kThreads, 1) exp_tc_kernel(const __grid_consta
                                    abort_flag);
                     if (!ok) break;
                     uint8_t *A = sm + (size_t)slot * C::kStage, *B = A + kBytesA;
-                    uint64_t *bar = &bars->full[slot];
-                    const bool second = KIND == kDaMlp && st >= j.steps1;
-                    mbar_arrive_expect_tx(
-                        bar, kBytesA + (second ? C::N2 * kStepK * 2 : C::N1 * kStepK * 2));
+                    const bool second = C::kTwo && st >= j.steps1;
+                    if (rank == 0)
+                        mbar_arrive_expect_tx(&bars->full[slot],
+                                              CG * (kBytesA + (second ? C::kB2 : C::kB1)));
+                    const uint32_t bar = CG == 2 ? mapa_u32(&bars->full[slot], 0)
+                                                 : smem_u32(&bars->full[slot]);
+                    auto box2 = [&](uint8_t *dst, const CUtensorMap *m, int x, int y) {
+                        if constexpr (CG == 2) tma_g2s_2d_pair(dst, m, x, y, bar);
+                        else tma_g2s_2d(dst, m, x, y, &bars->full[slot]);
+                    };
+                    auto box3 = [&](uint8_t *dst, const CUtensorMap *m, int x, int y) {
+                        if constexpr (CG == 2) tma_g2s_3d_pair(dst, m, x, y, j.expert, bar);
+                        else tma_g2s_3d(dst, m, x, y, j.expert, &bars->full[slot]);
+                    };
                     const int k = (second ? st - j.steps1 : st) * kStepK;
+                    // this CTA's first column of B in a phase of N columns
+                    const int n1 = j.col0 + rank * (C::N1 / CG);
                     if constexpr (C::kGrad) {
 #pragma unroll
                         for (int i = 0; i < kRowsA / 64; ++i)
-                            tma_g2s_2d(A + i * kBlk, &a.a, j.m0 + i * 64, row + k, bar);
+                            box2(A + i * kBlk, &a.a, j.m0 + i * 64, row + k);
 #pragma unroll
-                        for (int i = 0; i < C::NB / 64; ++i)
-                            tma_g2s_2d(B + i * kBlk, &a.b, j.col0 + i * 64, row + k, bar);
-                    } else {
-                        tma_g2s_2d(A, second ? &a.a2 : &a.a, k, row, bar);
-                        if (KIND == kDx || second) {
-                            constexpr int n = (KIND == kDx ? C::N1 : C::N2) / 64;
+                        for (int i = 0; i < C::N1 / CG / 64; ++i)
+                            box2(B + i * kBlk, &a.b, n1 + i * 64, row + k);
+                    } else if (!second) {
+                        box2(A, &a.a, k, row);
+                        if constexpr (C::kBMn1) {
 #pragma unroll
-                            for (int i = 0; i < n; ++i)
-                                tma_g2s_3d(B + i * kBlk, second ? &a.b2 : &a.b, j.col0 + i * 64, k,
-                                           j.expert, bar);
-                        } else if constexpr (GATED) {
-                            // the tile's gate rows, then its up rows
-                            tma_g2s_3d(B, &a.b, k, j.col0, j.expert, bar);
-                            tma_g2s_3d(B + C::kBytesB / 2, &a.b, k, j.col0 + s.h, j.expert, bar);
+                            for (int i = 0; i < C::N1 / CG / 64; ++i)
+                                box3(B + i * kBlk, &a.b, n1 + i * 64, k);
+                        } else if constexpr (KIND == kFirst && GATED) {
+                            // the tile's gate rows, then its up rows: one each
+                            // for a pair's CTAs
+                            if constexpr (CG == 2) {
+                                box3(B, &a.b, k, j.col0 + rank * s.h);
+                            } else {
+                                box3(B, &a.b, k, j.col0);
+                                box3(B + C::kB1 / 2, &a.b, k, j.col0 + s.h);
+                            }
                         } else {
-                            tma_g2s_3d(B, &a.b, k, j.col0, j.expert, bar);
+                            box3(B, &a.b, k, n1);
+                        }
+                    } else {
+                        box2(A, &a.a2, k, row);
+                        if constexpr (GATED && CG == 1) {
+                            box3(B, &a.b2, k, j.col0);
+                            box3(B + C::kB2 / 2, &a.b2, k, j.col0 + s.h);
+                        } else {
+                            box3(B, &a.b2, k,
+                                 j.col0 + (GATED ? rank * s.h : rank * (C::N2 / CG)));
                         }
                     }
                 }
             }
+            // no copy in flight at teardown: rank 0's barriers count both
+            // CTAs' copies (the cluster barrier below holds the other back),
+            // and the other CTA sees the last of its slots released, so that
+            // no arrival reaches it after it is gone
+            for (uint32_t f = fill > (uint32_t)C::kStages ? fill - C::kStages : 0; f < fill; ++f)
+                mbar_wait_drain(rank == 0 ? &bars->full[f % C::kStages]
+                                          : &bars->empty[f % C::kStages],
+                                (f / C::kStages) & 1, c.err);
         }
-        // no copy in flight at teardown
-        for (uint32_t f = fill > (uint32_t)C::kStages ? fill - C::kStages : 0; f < fill; ++f)
-            mbar_wait_drain(&bars->full[f % C::kStages], (f / C::kStages) & 1, c.err);
     } else if (warp == 1) {
         // ================================================ MMA issuer
-        if (lane == 0) {
-            constexpr bool kBf = sizeof(T) == 2 && !__is_same(T, __half);
-            constexpr uint32_t id1 = kBf ? idesc_bf16(128, C::N1, C::kAMn, C::kBMn)
-                                         : idesc_f16(128, C::N1, C::kAMn, C::kBMn);
-            constexpr uint32_t id2 = kBf ? idesc_bf16(128, C::N2 ? C::N2 : 64, false, true)
-                                         : idesc_f16(128, C::N2 ? C::N2 : 64, false, true);
+        if (lane == 0 && rank == 0) {
+            constexpr bool kBf = !__is_same(T, __half);
+            constexpr uint32_t bf = kBf ? idesc_bf16(128, 64, false, false) -
+                                              idesc_f16(128, 64, false, false)
+                                        : 0;
+            constexpr uint32_t id1 = idesc_f16(kRowsA * CG, C::N1, C::kAMn, C::kBMn1) + bf;
+            constexpr uint32_t id2 = idesc_f16(kRowsA * CG, C::N2 ? C::N2 : 64, false, false) + bf;
             const uint64_t dA = smem_desc(smem_u32(sm), C::kAMn ? kBlk : 16, 1024, kSwz128);
-            const uint64_t dB1 = smem_desc(smem_u32(sm + kBytesA), C::kBMn ? kBlk : 16, 1024,
+            const uint64_t dB1 = smem_desc(smem_u32(sm + kBytesA), C::kBMn1 ? kBlk : 16, 1024,
                                            kSwz128);
-            const uint64_t dB2 = smem_desc(smem_u32(sm + kBytesA), kBlk, 1024, kSwz128);
+            const uint64_t dB2 = smem_desc(smem_u32(sm + kBytesA), 16, 1024, kSwz128);
+            auto product = [&](uint32_t d, uint64_t da, uint64_t db, uint32_t id, bool add) {
+                if constexpr (CG == 2) mma_f16_pair(d, da, db, id, add ? 1u : 0u);
+                else mma_f16(d, da, db, id, add ? 1u : 0u);
+            };
+            auto commit = [&](uint64_t *bar) {
+                if constexpr (CG == 2) mma_commit_pair(bar);
+                else mma_commit(bar);
+            };
+            auto free_wait = [&](int buf, uint32_t parity) {
+                if constexpr (CG == 2)
+                    return mbar_wait_cluster(&bars->accfree[buf], parity, c.err, abort_flag);
+                else
+                    return mbar_wait(&bars->accfree[buf], parity, c.err, abort_flag);
+            };
             uint32_t use = 0, tile = 0;
             bool ok = true;
-            int idx = blockIdx.x;
-            Job nxt = idx < total ? job_of<KIND, GATED>(a, idx) : Job{};
-            for (; idx < total && ok; idx += gridDim.x, ++tile) {
+            int idx = first;
+            Job nxt = idx < total ? job_of<KIND, GATED, CG>(a, idx, 0) : Job{};
+            for (; idx < total && ok; idx += stride, ++tile) {
                 const Job j = nxt;
-                if (idx + (int)gridDim.x < total) nxt = job_of<KIND, GATED>(a, idx + gridDim.x);
+                if (idx + stride < total) nxt = job_of<KIND, GATED, CG>(a, idx + stride, 0);
                 const int buf = tile & 1;
-                if (!mbar_wait(&bars->accfree[buf], ((tile >> 1) & 1) ^ 1, c.err, abort_flag)) break;
+                if (!free_wait(buf, ((tile >> 1) & 1) ^ 1)) break;
                 tc_fence_after();
-                const uint32_t acc = tmem + buf * 256;
                 const int steps = j.steps1 + j.steps2;
                 for (int st = 0; st < steps; ++st, ++use) {
-                    const int slot = use % C::kStages;
-                    if (!mbar_wait(&bars->full[slot], (use / C::kStages) & 1, c.err, abort_flag)) {
-                        ok = false;
-                        break;
+                    const bool second = C::kTwo && st >= j.steps1;
+                    // the single phase-2 accumulator: the tile before is read
+                    if (C::kTwo && GATED && st == j.steps1 && tile > 0) {
+                        ok = free_wait((tile - 1) & 1, ((tile - 1) >> 1) & 1);
+                        if (!ok) break;
+                        tc_fence_after();
                     }
+                    const int slot = use % C::kStages;
+                    ok = mbar_wait(&bars->full[slot], (use / C::kStages) & 1, c.err, abort_flag);
+                    if (!ok) break;
                     tc_fence_after();
                     const uint32_t off = (uint32_t)(slot * C::kStage) >> 4;
-                    const bool second = KIND == kDaMlp && st >= j.steps1;
-                    const bool fresh = st == 0 || (KIND == kDaMlp && st == j.steps1);
+                    const bool fresh = st == 0 || (C::kTwo && st == j.steps1);
 #pragma unroll
                     for (int kk = 0; kk < kStepK / 16; ++kk) {
                         const uint64_t da = dA + off + (uint32_t)(kk * (C::kAMn ? 2048 : 32) >> 4);
                         if (second)
-                            mma_f16(acc + C::N1, da, dB2 + off + (uint32_t)(kk * 2048 >> 4), id2,
-                                    fresh && kk == 0 ? 0u : 1u);
+                            product(tmem + C::col2(tile), da, dB2 + off + (uint32_t)(kk * 32 >> 4),
+                                    id2, !fresh || kk > 0);
                         else
-                            mma_f16(acc, da,
-                                    dB1 + off + (uint32_t)(kk * (C::kBMn ? 2048 : 32) >> 4), id1,
-                                    fresh && kk == 0 ? 0u : 1u);
+                            product(tmem + C::col1(tile), da,
+                                    dB1 + off + (uint32_t)(kk * (C::kBMn1 ? 2048 : 32) >> 4), id1,
+                                    !fresh || kk > 0);
                     }
-                    mma_commit(&bars->empty[slot]);
+                    commit(&bars->empty[slot]);
                 }
-                if (ok) mma_commit(&bars->accfull[buf]);
+                if (ok) commit(&bars->accfull[buf]);
             }
-            mma_commit(&bars->done);
+            if constexpr (CG == 2) mma_commit_pair_local(&bars->done);
+            else mma_commit(&bars->done);
             mbar_wait_drain(&bars->done, 0, c.err);   // no MMA in flight at teardown
         }
     } else {
@@ -294,8 +369,8 @@ __global__ void __launch_bounds__(kThreads, 1) exp_tc_kernel(const __grid_consta
         const int q = warp & 3, hf = (warp - 2) >> 2, m = q * 32 + lane;
         const uint32_t lane_base = (uint32_t)(q * 32) << 16;
         uint32_t tile = 0;
-        for (int idx = blockIdx.x; idx < total; idx += gridDim.x, ++tile) {
-            const Job j = job_of<KIND, GATED>(a, idx);
+        for (int idx = first; idx < total; idx += stride, ++tile) {
+            const Job j = job_of<KIND, GATED, CG>(a, idx, rank);
             const int buf = tile & 1;
             const bool none = !C::kGrad && j.expert >= s.K;
             const bool valid = m < j.valid;
@@ -312,7 +387,9 @@ __global__ void __launch_bounds__(kThreads, 1) exp_tc_kernel(const __grid_consta
                                                    abort_flag)))
                 break;
             tc_fence_after();
-            const uint32_t acc = tmem + buf * 256 + lane_base;
+            // column 0 of the (last phase's) accumulator, and q's
+            const uint32_t acc = tmem + (C::kTwo ? C::col2(tile) : C::col1(tile)) + lane_base;
+            const uint32_t accq = tmem + C::col1(tile) + lane_base;
             const bool has = j.steps1 > 0;   // otherwise the accumulators were not written
             float part = 0.f;
             constexpr int kHalf = C::NB / 2;
@@ -321,9 +398,8 @@ __global__ void __launch_bounds__(kThreads, 1) exp_tc_kernel(const __grid_consta
                 uint32_t r0[32], r1[32], r2[32];
                 __syncwarp();   // the loads below are warp-wide
                 tmem_ld32(acc + c0, r0);
-                if constexpr (KIND == kFirst && GATED) tmem_ld32(acc + 128 + c0, r1);
-                if constexpr (KIND == kDaMlp && GATED) tmem_ld32(acc + 64 + c0, r1);
-                if constexpr (KIND == kDaMlp) tmem_ld32(acc + C::N1 + c0, r2);
+                if constexpr (GATED) tmem_ld32(acc + 128 + c0, r1);
+                if constexpr (C::kTwo) tmem_ld32(accq + c0, r2);
                 tmem_ld_wait();
 #pragma unroll
                 for (int v = 0; v < 4; ++v) {
@@ -349,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1) exp_tc_kernel(const __grid_consta
                         }
                     } else if constexpr (KIND == kDaLin || KIND == kDaMlp) {
                         const int width = s.mlp ? s.h : s.o;
-                        if (none || col >= width) continue;
+                        if (none || j.valid <= 0 || col >= width) continue;
                         T *da = (T *)c.da + row * s.first() + col;
                         T *hs = (T *)c.hid + row * s.h + col;
                         float d1[8], d2[8], h8[8];
@@ -365,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1) exp_tc_kernel(const __grid_consta
 #pragma unroll
                             for (int i = 0; i < 8; ++i) {
                                 float f, df;
-                                act_both<ACT>(x[i] + b8[i], f, df);
+                                act_fast<ACT>(x[i] + b8[i], f, df);
                                 float up = 1.f, qq;
                                 if constexpr (KIND == kDaMlp) qq = __uint_as_float(r2[v * 8 + i]);
                                 else qq = q8[i];
@@ -405,12 +481,18 @@ __global__ void __launch_bounds__(kThreads, 1) exp_tc_kernel(const __grid_consta
                                     float u8[8] = {};
                                     if (b) load8(b + width, a.vec_bias, u8);
 #pragma unroll
-                                    for (int i = 0; i < 8; ++i)
-                                        x[i] = act_of<ACT>(x[i]) *
-                                               (__uint_as_float(r1[v * 8 + i]) + u8[i]);
+                                    for (int i = 0; i < 8; ++i) {
+                                        float f, df;
+                                        act_fast<ACT>(x[i], f, df);
+                                        x[i] = f * (__uint_as_float(r1[v * 8 + i]) + u8[i]);
+                                    }
                                 } else {
 #pragma unroll
-                                    for (int i = 0; i < 8; ++i) x[i] = act_of<ACT>(x[i]);
+                                    for (int i = 0; i < 8; ++i) {
+                                        float f, df;
+                                        act_fast<ACT>(x[i], f, df);
+                                        x[i] = f;
+                                    }
                                 }
                             }
                             if (s.mlp) {
@@ -439,12 +521,20 @@ __global__ void __launch_bounds__(kThreads, 1) exp_tc_kernel(const __grid_consta
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->accfree[buf]);
+            if (lane == 0) {
+                if constexpr (CG == 2) mbar_arrive_cluster(mapa_u32(&bars->accfree[buf], 0));
+                else mbar_arrive(&bars->accfree[buf]);
+            }
         }
     }
     tc_fence_before();
-    __syncthreads();
-    if (warp == 1) tmem_dealloc(tmem, 512);
+    if constexpr (CG == 2) cluster_sync_all();
+    else __syncthreads();
+    tc_fence_after();
+    if (warp == 1) {
+        if constexpr (CG == 2) tmem_dealloc_pair(tmem, 512);
+        else tmem_dealloc(tmem, 512);
+    }
 }
 
 // ------------------------------------------------------------- host side
@@ -490,9 +580,9 @@ struct Maps {
     }
 };
 
-template <typename T, int KIND, int ACT, bool GATED>
+template <typename T, int KIND, int ACT, bool GATED, int CG>
 cudaError_t launch_kind(const ExpCall &c, cudaStream_t st) {
-    using C = Cfg<KIND, GATED>;
+    using C = Cfg<KIND, GATED, CG>;
     const ExpShape &s = c.s;
     Args a;
     a.c = c;
@@ -501,19 +591,21 @@ cudaError_t launch_kind(const ExpCall &c, cudaStream_t st) {
     switch (KIND) {
         case kFirst:
         case kDaLin:
-        case kDaMlp:
             width = s.mlp ? s.h : s.o;
             maps.make(&a.a, c.xrows, s.d, c.point_rows, 0, kRowsA);
-            maps.make(&a.b, c.w1, s.d, s.first(), s.K, GATED ? C::N1 / 2 : C::N1);
-            if (KIND == kDaMlp) {
-                maps.make(&a.a2, c.dyrows, s.o, c.point_rows, 0, kRowsA);
-                maps.make(&a.b2, c.w2, s.h, s.o, s.K, kStepK);
-            }
+            maps.make(&a.b, c.w1, s.d, s.first(), s.K, GATED ? 128 : C::N1 / CG);
+            break;
+        case kDaMlp:
+            width = s.h;
+            maps.make(&a.a, c.dyrows, s.o, c.point_rows, 0, kRowsA);
+            maps.make(&a.b, c.w2, s.h, s.o, s.K, kStepK);
+            maps.make(&a.a2, c.xrows, s.d, c.point_rows, 0, kRowsA);
+            maps.make(&a.b2, c.w1, s.d, s.first(), s.K, GATED ? 128 : C::N2 / CG);
             break;
         case kSecond:
             width = s.o;
             maps.make(&a.a, c.hid, s.h, c.max_rows, 0, kRowsA);
-            maps.make(&a.b, c.w2, s.h, s.o, s.K, C::N1);
+            maps.make(&a.b, c.w2, s.h, s.o, s.K, C::N1 / CG);
             break;
         case kDx:
             width = s.d;
@@ -535,35 +627,75 @@ cudaError_t launch_kind(const ExpCall &c, cudaStream_t st) {
     }
     if (!maps.ok) return cudaErrorNotSupported;
     a.ntn = (width + C::NB - 1) / C::NB;
-    a.ntm = (mrows + kRowsA - 1) / kRowsA;
+    a.ntm = (mrows + C::kTileRows - 1) / C::kTileRows;
     const void *bias = KIND == kSecond ? c.b2 : c.b1;
     a.vec_bias = ((uintptr_t)bias & 15) == 0;
     a.vec_res = ((uintptr_t)c.res & 15) == 0;
     const int64_t most = C::kGrad ? (int64_t)s.K * a.ntm * a.ntn : (int64_t)c.rt.max_tiles * a.ntn;
     if (most > 0x7fff0000) return cudaErrorNotSupported;
-    cudaError_t e = cudaFuncSetAttribute(exp_tc_kernel<T, KIND, ACT, GATED>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const auto kernel = exp_tc_kernel<T, KIND, ACT, GATED, CG>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)C::kSmem);
     if (e != cudaSuccess) return e;
-    const unsigned grid = (unsigned)(most < kSms ? most : kSms);
-    exp_tc_kernel<T, KIND, ACT, GATED><<<grid, kThreads, C::kSmem, st>>>(a);
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    if (CG == 2) {
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim = {2, 1, 1};
+        cfg.numAttrs = 1;
+    }
+    // one wave: as many pairs as can be resident (a GPC with an odd number of
+    // SMs leaves one out)
+    cfg.gridDim = dim3(kSms);
+    int wave = kSms;
+    if (CG == 2) {
+        static int resident = 0;
+        if (!resident) {
+            int n = 0;
+            e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+            if (e != cudaSuccess) return e;
+            resident = n < 1 ? 2 : 2 * n;
+        }
+        wave = resident < kSms ? resident : kSms;
+    }
+    const int64_t ctas = most * CG;
+    cfg.gridDim = dim3((unsigned)(ctas < wave ? ctas : wave));
+    e = cudaLaunchKernelEx(&cfg, kernel, a);
+    if (e != cudaSuccess) return e;
     note_launches(1);
     return cudaGetLastError();
+}
+
+// Products whose rows are points run in pairs when the segments are long
+// enough (kExpPairRows); a weight gradient when its own rows fill pairs too.
+template <typename T, int KIND, int ACT, bool GATED>
+cudaError_t launch_rows(const ExpCall &c, cudaStream_t st) {
+    return c.rt.tile_rows == 2 * kRowsA ? launch_kind<T, KIND, ACT, GATED, 2>(c, st)
+                                        : launch_kind<T, KIND, ACT, GATED, 1>(c, st);
+}
+template <typename T, int KIND> cudaError_t launch_grad(const ExpCall &c, cudaStream_t st) {
+    const int tiles = ((KIND == kDw2 ? c.s.o : c.s.first()) + kRowsA - 1) / kRowsA;
+    return c.rt.tile_rows == 2 * kRowsA && (tiles % 2 == 0 || tiles > 8) ? launch_kind<T, KIND, GMM_ACT_NONE, false, 2>(c, st)
+                                       : launch_kind<T, KIND, GMM_ACT_NONE, false, 1>(c, st);
 }
 
 template <typename T, int ACT, bool GATED>
 cudaError_t run_tc(const ExpCall &c, bool backward, cudaStream_t st) {
     cudaError_t e;
     if (!backward) {
-        e = launch_kind<T, kFirst, ACT, GATED>(c, st);
-        if (e == cudaSuccess && c.s.mlp) e = launch_kind<T, kSecond, GMM_ACT_NONE, false>(c, st);
+        e = launch_rows<T, kFirst, ACT, GATED>(c, st);
+        if (e == cudaSuccess && c.s.mlp) e = launch_rows<T, kSecond, GMM_ACT_NONE, false>(c, st);
         return e;
     }
-    if (c.s.mlp) e = launch_kind<T, kDaMlp, ACT, GATED>(c, st);
-    else e = launch_kind<T, kDaLin, ACT, false>(c, st);
-    if (e == cudaSuccess) e = launch_kind<T, kDx, GMM_ACT_NONE, false>(c, st);
-    if (e == cudaSuccess) e = launch_kind<T, kDw1, GMM_ACT_NONE, false>(c, st);
-    if (e == cudaSuccess && c.s.mlp) e = launch_kind<T, kDw2, GMM_ACT_NONE, false>(c, st);
+    if (c.s.mlp) e = launch_rows<T, kDaMlp, ACT, GATED>(c, st);
+    else e = launch_rows<T, kDaLin, ACT, false>(c, st);
+    if (e == cudaSuccess) e = launch_rows<T, kDx, GMM_ACT_NONE, false>(c, st);
+    if (e == cudaSuccess) e = launch_grad<T, kDw1>(c, st);
+    if (e == cudaSuccess && c.s.mlp) e = launch_grad<T, kDw2>(c, st);
     return e;
 }
 
@@ -591,9 +723,8 @@ cudaError_t launch_exp_tc(const ExpCall &c, bool backward, cudaStream_t s) {
 
 // Partial sums of dresp per row: two halves of each column tile.
 int exp_tc_resp_parts(const ExpShape &s) {
-    if (!s.mlp) return 2 * ((s.o + Cfg<kDaLin, false>::NB - 1) / Cfg<kDaLin, false>::NB);
-    const int nb = s.gated ? Cfg<kDaMlp, true>::NB : Cfg<kDaMlp, false>::NB;
-    return 2 * ((s.h + nb - 1) / nb);
+    const int nb = s.mlp ? 128 : 256;
+    return 2 * (((s.mlp ? s.h : s.o) + nb - 1) / nb);
 }
 
 }  // namespace gmmb

@@ -244,6 +244,11 @@ LINEAR = [
     (520, 256, 512, 1, 0, "bf16", "none", {"bias": False}),
     (300, 128, 128, 64, 8, "bf16", "gelu", {}),                           # short segments
     (700, 64, 40, 300, 2, "f16", "silu", {"use": [0, 299, 17]}),          # unused experts
+    (1000, 72, 264, 2, 2, "bf16", "silu", {"cut": 0.1, "res": True}),     # pairs of row tiles
+    (900, 136, 600, 2, 1, "f16", "none", {"cut": 0.3}),
+    (385, 64, 64, 1, 0, "bf16", "gelu", {"res": True}),
+    (5000, 16, 8, 3, 8, "bf16", "none", {"cut": 0.5}),                    # 40000 pairs
+    (600, 16, 8, 2000, 2, "f16", "none", {"cut": 0.1}),                   # many experts
 ]
 
 
@@ -268,6 +273,9 @@ MLP = [
     (300, 64, 64, 64, 64, 8, "f16", "gelu", False, {"bias": False}),
     (150, 50, 60, 70, 6, 3, "f32", "gelu", True, {"cut": 0.2}),
     (600, 64, 72, 64, 200, 2, "bf16", "none", False, {"use": [3, 198, 199], "resp": False}),
+    (1000, 72, 136, 200, 2, 2, "bf16", "silu", True, {"cut": 0.1, "res": True}),   # pairs of tiles
+    (700, 200, 264, 72, 2, 2, "f16", "gelu", False, {}),
+    (641, 64, 320, 64, 1, 0, "bf16", "silu", True, {"bias": False}),
 ]
 
 
