@@ -49,7 +49,7 @@ int path_of(const ExpShape &p, bool, uint32_t flags) {
 }
 
 struct Layout {
-    size_t cnt, seg, tile_expert, pair_at, ntiles, row_pair, hist, hid, da, xrows, dyrows, slots, rpart, total;
+    size_t cnt, seg, tile_expert, pair_at, ntiles, row_pair, hist, hid, da, xrows, dyrows, slots, rpart, colpart, total;
     int64_t max_rows;
     int max_tiles, nrpart;
     size_t esize;
@@ -86,6 +86,13 @@ Layout layout_of(const ExpShape &p, bool backward, int path) {
     const int wide = !backward ? p.o : (p.d > p.o ? p.d : p.o);
     take(L.slots, p.direct() ? 0 : (size_t)p.P * wide * 4);
     take(L.rpart, backward ? (size_t)L.max_rows * L.nrpart * 4 : 0);
+    size_t cols = 0;   // partial bias gradients, one bias at a time
+    if (backward && path == 2) {
+        cols = (size_t)exp_colsum_slices(p, p.first()) * p.first();
+        const size_t c2 = (size_t)exp_colsum_slices(p, p.o) * p.o;
+        if (p.mlp && c2 > cols) cols = c2;
+    }
+    take(L.colpart, cols * p.K * 4);
     L.total = o;
     return L;
 }
@@ -116,6 +123,7 @@ ExpCall make_call(const ExpShape &p, const Layout &L, void *ws, const int32_t *i
     c.point_rows = p.dense ? p.N : L.max_rows;
     c.slots = (float *)(b + L.slots);
     c.rpart = (float *)(b + L.rpart);
+    c.colpart = (float *)(b + L.colpart);
     c.max_rows = L.max_rows;
     c.nrpart = L.nrpart;
     c.esize = L.esize;

@@ -95,7 +95,7 @@ struct ExpCall {
     // cores; the arrays themselves in the dense form), and how many
     void *xrows, *dyrows;
     int64_t point_rows;
-    float *slots, *rpart;
+    float *slots, *rpart, *colpart;
     int64_t max_rows;
     int nrpart;         // partial sums of dresp per row
     size_t esize;       // bytes per element of hid and da
@@ -175,6 +175,7 @@ cudaError_t launch_exp_combine(const ExpCall &c, bool backward, cudaStream_t s);
 // dresp from its partial sums (and <dy, b2>); column sums of da and g dy
 cudaError_t launch_exp_dresp(const ExpCall &c, cudaStream_t s);
 cudaError_t launch_exp_bias_grads(const ExpCall &c, cudaStream_t s);
+int exp_colsum_slices(const ExpShape &s, int width);
 // experts_simt.cu: the products on CUDA cores
 cudaError_t launch_exp_simt(const ExpCall &c, bool backward, cudaStream_t s);
 // experts_tc.cu: on the tensor cores (16-bit types, widths multiples of 8)

@@ -70,7 +70,10 @@ template <int KIND, bool GATED, int CG> struct Cfg {
     static constexpr int kBytesB = kB1 > kB2 ? kB1 : kB2;
     static constexpr int kStage = kBytesA + kBytesB;
     static constexpr int kStages = 192 * 1024 / kStage;
-    static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + 256;
+    // what an epilogue warp keeps of its columns' biases (gate and up), fp32
+    static constexpr bool kBias = !kGrad && KIND != kDx;
+    static constexpr int kBiasBytes = kBias ? 8 * 2 * 128 * 4 : 0;
+    static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + kBiasBytes + 256;
     static constexpr bool kAMn = kGrad;
     static constexpr bool kBMn1 = kGrad || KIND == kDx || kTwo;
     static constexpr int kTileRows = kRowsA * CG;
@@ -87,7 +90,7 @@ struct Args {
     ExpCall c;
     CUtensorMap a, b, a2, b2;   // phase 1 and phase 2 operands
     int ntn, ntm;               // column tiles; row tiles of one expert's dW
-    int vec_bias, vec_res;      // biases / residual may be read 16 bytes at a time
+    int vec_res;                // the residual may be read 16 bytes at a time
 };
 
 struct Bars {
@@ -137,18 +140,18 @@ __device__ __forceinline__ Job job_of(const Args &a, int idx, int rank) {
     return j;
 }
 
-// Eight consecutive elements as floats.
-template <typename T>
-__device__ __forceinline__ void load8(const T *p, bool vec, float (&v)[8]) {
-    if (vec) {
-        const uint4 w = *reinterpret_cast<const uint4 *>(p);
-        const T *e = reinterpret_cast<const T *>(&w);
+// Eight consecutive elements, raw, and as floats.
+template <typename T> __device__ __forceinline__ uint4 load8(const T *p, bool vec) {
+    if (vec) return *reinterpret_cast<const uint4 *>(p);
+    __align__(16) T e[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = to_float(e[i]);
-    } else {
+    for (int i = 0; i < 8; ++i) e[i] = p[i];
+    return *reinterpret_cast<const uint4 *>(e);
+}
+template <typename T> __device__ __forceinline__ void unpack8(const uint4 &w, float (&v)[8]) {
+    const T *e = reinterpret_cast<const T *>(&w);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = to_float(p[i]);
-    }
+    for (int i = 0; i < 8; ++i) v[i] = to_float(e[i]);
 }
 template <typename T> __device__ __forceinline__ uint32_t pack2(float x, float y);
 template <> __device__ __forceinline__ uint32_t pack2<__half>(float x, float y) {
@@ -165,13 +168,20 @@ __device__ __forceinline__ void store8(T *p, const float (&v)[8]) {
                                                pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7]));
 }
 
+__device__ __forceinline__ void store8(float *p, const float (&v)[8]) {
+    float4 *o = reinterpret_cast<float4 *>(p);
+    o[0] = make_float4(v[0], v[1], v[2], v[3]);
+    o[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+
 template <typename T, int KIND, int ACT, bool GATED, int CG>
 __global__ void __launch_bounds__(kThreads, 1) exp_tc_kernel(const __grid_constant__ Args a) {
     using C = Cfg<KIND, GATED, CG>;
     extern __shared__ uint8_t raw_smem[];
     uint8_t *sm = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~(uintptr_t)1023);
-    Bars *bars = reinterpret_cast<Bars *>(sm + (size_t)C::kStages * C::kStage);
+    float *bias_sm = reinterpret_cast<float *>(sm + (size_t)C::kStages * C::kStage);
+    Bars *bars = reinterpret_cast<Bars *>(sm + (size_t)C::kStages * C::kStage + C::kBiasBytes);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     static_assert(sizeof(Bars) + 8 <= 256 && C::kStages <= 8, "barrier block");
@@ -368,6 +378,18 @@ __global__ void __launch_bounds__(kThreads, 1) exp_tc_kernel(const __grid_consta
         // ================================================ epilogue
         const int q = warp & 3, hf = (warp - 2) >> 2, m = q * 32 + lane;
         const uint32_t lane_base = (uint32_t)(q * 32) << 16;
+        constexpr int kHalf = C::NB / 2;
+        float *gate_b = bias_sm + (warp - 2) * 256, *up_b = gate_b + 128;
+        // columns of the result, and of the rows that are added or multiplied
+        const int width = KIND == kDw2                        ? s.h
+                          : KIND == kDw1 || KIND == kDx       ? s.d
+                          : KIND == kSecond                   ? s.o
+                          : s.mlp                             ? s.h
+                                                              : s.o;
+        // this kind reads a row of another array beside the accumulators
+        const bool with_res = (KIND == kSecond || (KIND == kFirst && !s.mlp)) && s.direct() && c.res;
+        const bool with_aux = KIND == kDaLin || with_res;
+        const bool aux_vec = KIND == kDaLin || a.vec_res;
         uint32_t tile = 0;
         for (int idx = first; idx < total; idx += stride, ++tile) {
             const Job j = job_of<KIND, GATED, CG>(a, idx, rank);
@@ -382,6 +404,29 @@ __global__ void __launch_bounds__(kThreads, 1) exp_tc_kernel(const __grid_consta
                 tok = rt.token(pair);
                 if (c.resp) g = c.resp[pair];
             }
+            if constexpr (C::kBias) {
+                const T *b = (const T *)(KIND == kSecond ? c.b2 : c.b1);
+                if (b && !none) b += (size_t)j.expert * (KIND == kSecond ? s.o : s.first());
+#pragma unroll
+                for (int i = lane; i < kHalf; i += 32) {
+                    const int col = j.col0 + hf * kHalf + i;
+                    const bool in = b && !none && col < width;
+                    gate_b[i] = in ? to_float(b[col]) : 0.f;
+                    if (GATED) up_b[i] = in ? to_float(b[width + col]) : 0.f;
+                }
+            }
+            // the other array's row, 32 columns ahead of their use
+            const T *aux = (const T *)(KIND == kDaLin ? c.dy : c.res) + tok * width;
+            uint4 next[4];
+            auto fetch = [&](int c0) {
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const int col = j.col0 + c0 + v * 8;
+                    next[v] = make_uint4(0u, 0u, 0u, 0u);
+                    if (valid && col < width) next[v] = load8(aux + col, aux_vec);
+                }
+            };
+            if (with_aux) fetch(hf * kHalf);
             __syncwarp();
             if (!__all_sync(0xffffffffu, mbar_wait(&bars->accfull[buf], (tile >> 1) & 1, c.err,
                                                    abort_flag)))
@@ -392,125 +437,91 @@ __global__ void __launch_bounds__(kThreads, 1) exp_tc_kernel(const __grid_consta
             const uint32_t accq = tmem + C::col1(tile) + lane_base;
             const bool has = j.steps1 > 0;   // otherwise the accumulators were not written
             float part = 0.f;
-            constexpr int kHalf = C::NB / 2;
 #pragma unroll 1
             for (int c0 = hf * kHalf; c0 < (hf + 1) * kHalf; c0 += 32) {
                 uint32_t r0[32], r1[32], r2[32];
+                uint4 now[4];
                 __syncwarp();   // the loads below are warp-wide
                 tmem_ld32(acc + c0, r0);
                 if constexpr (GATED) tmem_ld32(acc + 128 + c0, r1);
                 if constexpr (C::kTwo) tmem_ld32(accq + c0, r2);
+                if (with_aux) {
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) now[v] = next[v];
+                    if (c0 + 32 < (hf + 1) * kHalf) fetch(c0 + 32);
+                }
                 tmem_ld_wait();
+                const float *gb = gate_b + (c0 - hf * kHalf), *ub = up_b + (c0 - hf * kHalf);
 #pragma unroll
                 for (int v = 0; v < 4; ++v) {
                     const int col = j.col0 + c0 + v * 8;
-                    float x[8];
+                    if (col >= width) continue;
+                    float x[8], b8[8], u8[8], o8[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] = has ? __uint_as_float(r0[v * 8 + i]) : 0.f;
+                    for (int i = 0; i < 8; ++i) {
+                        x[i] = has ? __uint_as_float(r0[v * 8 + i]) : 0.f;
+                        if constexpr (C::kBias) b8[i] = gb[v * 8 + i];
+                        if constexpr (GATED) u8[i] = ub[v * 8 + i];
+                    }
+                    if constexpr (KIND == kDaLin || KIND == kFirst || KIND == kSecond)
+                        if (with_aux) unpack8<T>(now[v], o8);
                     if constexpr (C::kGrad) {
                         const int M = KIND == kDw2 ? s.o : s.first();
-                        const int N = KIND == kDw2 ? s.h : s.d;
                         T *out = (T *)(KIND == kDw2 ? c.dw2 : c.dw1);
-                        if (j.m0 + m < M && col < N)
-                            store8(out + ((size_t)j.expert * M + j.m0 + m) * N + col, x);
+                        if (j.m0 + m < M)
+                            store8(out + ((size_t)j.expert * M + j.m0 + m) * width + col, x);
                     } else if constexpr (KIND == kDx) {
-                        if (valid && col < s.d) {
-                            if (s.direct()) {
-                                store8((T *)c.dx + tok * s.d + col, x);
-                            } else {
-                                float4 *o = reinterpret_cast<float4 *>(c.slots + pair * s.d + col);
-                                o[0] = make_float4(x[0], x[1], x[2], x[3]);
-                                o[1] = make_float4(x[4], x[5], x[6], x[7]);
-                            }
+                        if (valid) {
+                            if (s.direct()) store8((T *)c.dx + tok * width + col, x);
+                            else store8(c.slots + pair * width + col, x);
                         }
                     } else if constexpr (KIND == kDaLin || KIND == kDaMlp) {
-                        const int width = s.mlp ? s.h : s.o;
-                        if (none || j.valid <= 0 || col >= width) continue;
+                        if (none || j.valid <= 0) continue;
                         T *da = (T *)c.da + row * s.first() + col;
-                        T *hs = (T *)c.hid + row * s.h + col;
                         float d1[8], d2[8], h8[8];
-                        if (valid) {
-                            float b8[8] = {}, u8[8] = {}, q8[8];
-                            const T *b = (const T *)c.b1 + (size_t)j.expert * s.first() + col;
-                            if (c.b1) {
-                                load8(b, a.vec_bias, b8);
-                                if (GATED) load8(b + width, a.vec_bias, u8);
-                            }
-                            if constexpr (KIND == kDaLin)
-                                load8((const T *)c.dy + tok * s.o + col, true, q8);
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                float f, df;
-                                act_fast<ACT>(x[i] + b8[i], f, df);
-                                float up = 1.f, qq;
-                                if constexpr (KIND == kDaMlp) qq = __uint_as_float(r2[v * 8 + i]);
-                                else qq = q8[i];
-                                if constexpr (GATED) up = __uint_as_float(r1[v * 8 + i]) + u8[i];
-                                const float gq = g * qq, fu = f * up;
-                                part = fmaf(qq, fu, part);
-                                d1[i] = gq * up * df;
-                                d2[i] = gq * f;
-                                h8[i] = g * fu;
-                            }
-                        } else {
+                        for (int i = 0; i < 8; ++i) {
+                            float f, df, up = 1.f, qq;
+                            act_fast<ACT>(x[i] + b8[i], f, df);
+                            if constexpr (KIND == kDaMlp) qq = __uint_as_float(r2[v * 8 + i]);
+                            else qq = o8[i];
+                            if constexpr (GATED) up = __uint_as_float(r1[v * 8 + i]) + u8[i];
+                            const float gq = g * qq, fu = f * up;
                             // rows past the segment are zeros: the weight
                             // gradients contract over them
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) d1[i] = d2[i] = h8[i] = 0.f;
+                            part = fmaf(qq, fu, part);
+                            d1[i] = valid ? gq * up * df : 0.f;
+                            if constexpr (GATED) d2[i] = valid ? gq * f : 0.f;
+                            if constexpr (KIND == kDaMlp) h8[i] = valid ? g * fu : 0.f;
                         }
                         store8(da, d1);
-                        if constexpr (KIND == kDaMlp) {
-                            if constexpr (GATED) store8(da + width, d2);
-                            store8(hs, h8);
-                        }
+                        if constexpr (GATED) store8(da + width, d2);
+                        if constexpr (KIND == kDaMlp) store8((T *)c.hid + row * width + col, h8);
                     } else {
-                        const int width = KIND == kSecond ? s.o : s.mlp ? s.h : s.o;
-                        if (!valid || col >= width) continue;
-                        if (KIND == kFirst && s.mlp && none) continue;
-                        const T *b = (const T *)(KIND == kSecond ? c.b2 : c.b1);
-                        if (b && !none) {
-                            b += (size_t)j.expert * (KIND == kSecond ? s.o : s.first()) + col;
-                            float b8[8];
-                            load8(b, a.vec_bias, b8);
+                        if (!valid) continue;
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) x[i] += b8[i];
-                        }
-                        if constexpr (KIND == kFirst) {
-                            if (!none) {
-                                if constexpr (GATED) {
-                                    float u8[8] = {};
-                                    if (b) load8(b + width, a.vec_bias, u8);
-#pragma unroll
-                                    for (int i = 0; i < 8; ++i) {
-                                        float f, df;
-                                        act_fast<ACT>(x[i], f, df);
-                                        x[i] = f * (__uint_as_float(r1[v * 8 + i]) + u8[i]);
-                                    }
-                                } else {
-#pragma unroll
-                                    for (int i = 0; i < 8; ++i) {
-                                        float f, df;
-                                        act_fast<ACT>(x[i], f, df);
-                                        x[i] = f;
-                                    }
-                                }
-                            }
-                            if (s.mlp) {
-                                // rounded to the type: the second product's operand
-                                store8((T *)c.hid + row * width + col, x);
-                                continue;
+                        for (int i = 0; i < 8; ++i) {
+                            x[i] += b8[i];
+                            if constexpr (KIND == kFirst) {
+                                float f, df;
+                                act_fast<ACT>(x[i], f, df);
+                                x[i] = f;
+                                if constexpr (GATED)
+                                    x[i] *= __uint_as_float(r1[v * 8 + i]) + u8[i];
                             }
                         }
-                        if (s.direct()) {
-                            float r8[8] = {};
-                            if (c.res) load8((const T *)c.res + tok * width + col, a.vec_res, r8);
+                        if (KIND == kFirst && s.mlp) {
+                            // rounded to the type: the second product's operand
+                            if (!none) store8((T *)c.hid + row * width + col, x);
+                        } else if (s.direct()) {
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) x[i] = none ? r8[i] : fmaf(g, x[i], r8[i]);
+                            for (int i = 0; i < 8; ++i) {
+                                const float r = with_res ? o8[i] : 0.f;
+                                x[i] = none ? r : fmaf(g, x[i], r);
+                            }
                             store8((T *)c.y + tok * width + col, x);
                         } else {
-                            float4 *o = reinterpret_cast<float4 *>(c.slots + pair * width + col);
-                            o[0] = make_float4(x[0], x[1], x[2], x[3]);
-                            o[1] = make_float4(x[4], x[5], x[6], x[7]);
+                            store8(c.slots + pair * width + col, x);
                         }
                     }
                 }
@@ -628,8 +639,6 @@ cudaError_t launch_kind(const ExpCall &c, cudaStream_t st) {
     if (!maps.ok) return cudaErrorNotSupported;
     a.ntn = (width + C::NB - 1) / C::NB;
     a.ntm = (mrows + C::kTileRows - 1) / C::kTileRows;
-    const void *bias = KIND == kSecond ? c.b2 : c.b1;
-    a.vec_bias = ((uintptr_t)bias & 15) == 0;
     a.vec_res = ((uintptr_t)c.res & 15) == 0;
     const int64_t most = C::kGrad ? (int64_t)s.K * a.ntm * a.ntn : (int64_t)c.rt.max_tiles * a.ntn;
     if (most > 0x7fff0000) return cudaErrorNotSupported;
