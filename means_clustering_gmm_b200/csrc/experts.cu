@@ -41,10 +41,11 @@ ExpShape make_shape(const gmm_expert_shape *s) {
     return p;
 }
 
-int path_of(const ExpShape &p, bool, uint32_t flags) {
+int path_of(const ExpShape &p, bool backward, uint32_t flags) {
     if (flags & GMM_FLAG_FORCE_SIMT) return 0;
     // tensor maps want rows of whole 16-byte units
     if (p.dt == GMM_F32 || p.d % 8 || p.h % 8 || p.o % 8) return 0;
+    if (!backward && p.N <= kExpFewPoints && p.P <= GMM_EXPERT_FEW_PAIRS) return 1;
     return 2;
 }
 
@@ -195,6 +196,7 @@ gmm_status forward(const gmm_expert_shape *shape, bool mlp, const void *X, const
     c.res = residual;
     c.resp = resp;
     c.y = Y;
+    if (path == 1) return launch_exp_few(c, s) == cudaSuccess ? GMM_OK : GMM_ERR_CUDA;
     if (launch_exp_route(c, s) != cudaSuccess) return GMM_ERR_CUDA;
     if (products(c, path, false, s) != cudaSuccess) return GMM_ERR_CUDA;
     if (!p.direct() && launch_exp_combine(c, false, s) != cudaSuccess) return GMM_ERR_CUDA;

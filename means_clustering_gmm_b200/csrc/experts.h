@@ -180,6 +180,11 @@ int exp_colsum_slices(const ExpShape &s, int width);
 cudaError_t launch_exp_simt(const ExpCall &c, bool backward, cudaStream_t s);
 // experts_tc.cu: on the tensor cores (16-bit types, widths multiples of 8)
 cudaError_t launch_exp_tc(const ExpCall &c, bool backward, cudaStream_t s);
+// experts_few.cu: the whole forward call for few points
+cudaError_t launch_exp_few(const ExpCall &c, cudaStream_t s);
+// Points up to which that form runs: its sums of 16 outputs of every point
+// stay in shared memory.
+constexpr int64_t kExpFewPoints = 64;
 int exp_tc_resp_parts(const ExpShape &s);
 
 }  // namespace gmmb

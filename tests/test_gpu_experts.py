@@ -249,6 +249,10 @@ LINEAR = [
     (385, 64, 64, 1, 0, "bf16", "gelu", {"res": True}),
     (5000, 16, 8, 3, 8, "bf16", "none", {"cut": 0.5}),                    # 40000 pairs
     (600, 16, 8, 2000, 2, "f16", "none", {"cut": 0.1}),                   # many experts
+    (64, 136, 72, 1, 0, "bf16", "gelu", {"res": True}),
+    (2, 1032, 4000, 1, 0, "f16", "silu", {"res": True}),
+    (64, 200, 40, 3, 4, "bf16", "silu", {"cut": 0.3, "res": True}),
+    (50, 64, 40, 3, 1, "bf16", "gelu", {"cut": 0.4, "res": True}),
 ]
 
 
@@ -263,6 +267,7 @@ MLP = [
     (1, 1, 1, 1, 1, 0, "f32", "silu", False, {}),
     (1, 64, 64, 64, 8, 2, "bf16", "silu", True, {"res": True}),
     (5, 72, 40, 24, 3, 2, "f16", "gelu", False, {"cut": 0.3}),
+    (1, 4096, 2048, 136, 9, 8, "bf16", "silu", True, {}),
     (16, 128, 64, 136, 64, 4, "bf16", "silu", True, {"bias": False, "res": True}),
     (31, 264, 104, 128, 5, 8, "f16", "none", True, {}),
     (33, 31, 29, 27, 3, 2, "bf16", "silu", True, {"cut": 0.2}),           # odd widths
@@ -276,6 +281,10 @@ MLP = [
     (1000, 72, 136, 200, 2, 2, "bf16", "silu", True, {"cut": 0.1, "res": True}),   # pairs of tiles
     (700, 200, 264, 72, 2, 2, "f16", "gelu", False, {}),
     (641, 64, 320, 64, 1, 0, "bf16", "silu", True, {"bias": False}),
+    (32, 520, 136, 40, 40, 8, "bf16", "silu", True, {"cut": 0.2, "res": True}),     # 256 pairs
+    (64, 64, 1032, 24, 2, 4, "f16", "gelu", False, {"res": True}),                  # 128 a expert
+    (64, 72, 40, 1000, 300, 4, "bf16", "silu", False, {"resp": False}),
+    (64, 64, 64, 64, 1, 0, "f16", "silu", True, {"res": True}),
 ]
 
 
@@ -363,10 +372,12 @@ def test_nan_stays_with_its_point(flags, N):
     assert g["dw1"][2].isnan().any()
 
 
-def test_same_expert_twice():
+@pytest.mark.parametrize("N", [1, 50, 200])
+def test_same_expert_twice(N):
     """Two entries that name one expert add up."""
-    s = inputs(8, 50, 64, 72, 64, 3, 2, "bf16", res=True)
+    s = inputs(8, N, 64, 72, 64, 3, 4, "bf16", res=True)
     s["ids"][:, 1] = s["ids"][:, 0]
+    s["ids"][::2, 3] = s["ids"][::2, 0]
     check(s, "silu")
 
 
