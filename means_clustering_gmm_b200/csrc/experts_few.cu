@@ -1,23 +1,27 @@
 // The experts' products for few points (16-bit types, widths multiples of 8,
-// at most GMM_EXPERT_FEW_PAIRS pairs): each used expert's weights are read
-// once, and that read is the bound.
+// at most kExpFewPoints points and GMM_EXPERT_FEW_PAIRS pairs): each used
+// expert's weights are read once, and that read is the bound.
 //
 //   few_first_kernel   a block is 16 or 32 rows of one expert's first weight;
 //                      the blocks of a pair whose expert an earlier pair
 //                      names leave at once.  All points of the expert are the
 //                      columns of one product.
-//   few_second_kernel  a cluster is 16 rows of the output for all points;
-//                      (expert, slice of h) units are dealt to its warps,
-//                      whose weighted sums are added up in a fixed order
-//                      through shared and distributed shared memory, with b2
-//                      and the residual: no array of per-pair results and no
-//                      third kernel.
+//   few_second_kernel  a cluster is 16 rows of the output for all points; its
+//                      warps share out the contraction indices of all used
+//                      experts evenly, and their weighted sums are added up
+//                      in a fixed order through shared and distributed shared
+//                      memory, with b2 and the residual: no array of per-pair
+//                      results and no third kernel.  It is launched under the
+//                      first one's tail and prefetches its part of W2 there.
 //
 // Weights go from global memory straight into mma.sync fragments (a lane
 // holds 8 consecutive elements of rows g and g + 8, 16 bytes each; the
-// contraction index is permuted the same way in both operands), because with
-// 1 to 32 columns the tensor cores wait for memory whatever form is used, and
-// a register fragment needs neither shared memory nor barriers on the way.
+// contraction index is permuted the same way in both operands): with 1 to 32
+// columns the tensor cores wait for memory whatever form is used, and a
+// register fragment needs neither shared memory nor barriers on the way.  A
+// ring of TMA stages was built instead and was slower (one point, 8 gated
+// experts of 2048-1024-2048: 33 us against 25): its stream alone, with the
+// products taken out, ran at 5.4 TB/s where coalesced loads run at 6.3.
 #include "experts.h"
 #include "tc_ptx.cuh"
 
@@ -29,6 +33,8 @@ using namespace tc;
 constexpr int kPairs = GMM_EXPERT_FEW_PAIRS;
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
+constexpr int kCols = 32;                     // points of one expert per pass
+constexpr int kSegs = kPairs + kPairs / kCols;
 static_assert(kPairs == kThreads, "one thread looks at one pair");
 
 template <typename T>
@@ -52,7 +58,6 @@ __device__ __forceinline__ void mma16<__nv_bfloat16>(float (&d)[4], const uint32
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-
 // 16 bytes of weights, read once: not kept in L1.
 __device__ __forceinline__ uint4 stream16(const void *p) {
     uint4 v;
@@ -62,48 +67,198 @@ __device__ __forceinline__ uint4 stream16(const void *p) {
     return v;
 }
 
-// acc[nt] += 16 weight rows x 8 points, over the 32-wide chunks c0, c0 + step,
-// .. of a contraction of K.  w0 / w1: rows g and g + 8 (NULL: zeros); x[nt]:
-// the row of point 8 nt + g (NULL: zeros).
+// acc[nt] += 16 weight rows x 8 points over the contraction indices [k0, k1)
+// (k0 a multiple of 32).  w0 / w1: rows g and g + 8; x[nt]: the row of point
+// 8 nt + g.  All are rows that exist (a lane without one of its own repeats
+// another's; its sums are not used), so whole chunks need no tests and cost
+// three loads and two products each.
 template <typename T, int NT, int U>
-__device__ __forceinline__ void stream_rows(float (&acc)[NT][4], const T *w0, const T *w1,
-                                            const T *const (&x)[NT], int K, int c0, int step,
-                                            int chunks) {
+__device__ __forceinline__ void stream_rows(float (&acc)[4][4], const T *w0, const T *w1,
+                                            const T *const (&x)[4], int k0, int k1) {
     const int t8 = (threadIdx.x & 3) * 8;
-    for (int c = c0; c < chunks; c += step * U) {
+    auto products = [&](const uint4 &a0, const uint4 &a1, const uint4 (&b)[NT]) {
+        const uint32_t lo[4] = {a0.x, a1.x, a0.y, a1.y};
+        const uint32_t hi[4] = {a0.z, a1.z, a0.w, a1.w};
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            mma16<T>(acc[n], lo, b[n].x, b[n].y);
+            mma16<T>(acc[n], hi, b[n].z, b[n].w);
+        }
+    };
+    int k = k0 + t8;
+    const int end = k1 + t8;
+    for (; k + 32 * U <= end; k += 32 * U) {
         uint4 a0[U], a1[U], b[U][NT];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int cc = c + u * step, k = cc * 32 + t8;
-            const bool in = cc < chunks && k < K;
-            a0[u] = a1[u] = make_uint4(0u, 0u, 0u, 0u);
-            if (in && w0) a0[u] = stream16(w0 + k);
-            if (in && w1) a1[u] = stream16(w1 + k);
+            a0[u] = stream16(w0 + k + u * 32);
+            a1[u] = stream16(w1 + k + u * 32);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                b[u][n] = make_uint4(0u, 0u, 0u, 0u);
-                if (in && x[n]) b[u][n] = *reinterpret_cast<const uint4 *>(x[n] + k);
-            }
+            for (int n = 0; n < NT; ++n)
+                b[u][n] = *reinterpret_cast<const uint4 *>(x[n] + k + u * 32);
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const uint32_t lo[4] = {a0[u].x, a1[u].x, a0[u].y, a1[u].y};
-            const uint32_t hi[4] = {a0[u].z, a1[u].z, a0[u].w, a1[u].w};
+        for (int u = 0; u < U; ++u) products(a0[u], a1[u], b[u]);
+    }
+    for (; k < end; k += 32) {
+        uint4 a0 = make_uint4(0u, 0u, 0u, 0u), a1 = a0, b[NT];
+        const bool in = k < k1;
+        if (in) {
+            a0 = stream16(w0 + k);
+            a1 = stream16(w1 + k);
+        }
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                mma16<T>(acc[n], lo, b[u][n].x, b[u][n].y);
-                mma16<T>(acc[n], hi, b[u][n].z, b[u][n].w);
+        for (int n = 0; n < NT; ++n) {
+            b[n] = make_uint4(0u, 0u, 0u, 0u);
+            if (in) b[n] = *reinterpret_cast<const uint4 *>(x[n] + k);
+        }
+        products(a0, a1, b);
+    }
+}
+
+// What the pairs name, in shared memory: the entries (pairs) sorted by expert
+// and, per run of at most 32 entries of one expert, a segment.
+struct Lists {
+    int ids[kPairs];        // expert of each pair, or -1
+    int start[kPairs];      // of a pair that names its expert first: its first entry
+    float weight[kPairs];   // of an entry
+    int2 seg[kSegs];        // expert, first entry | entries << 16
+    int16_t pair[kPairs];   // of an entry
+    int wsum[kWarps];
+    int segs;
+};
+
+// Threads 0..255, one per pair; the others only take part in the barriers.
+// ONCE: a pair that repeats its point's expert has no entry of its own; its
+// weight goes to the first one's.
+template <bool ONCE>
+__device__ __forceinline__ void make_lists(const ExpCall &c, Lists &L) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int P = (int)c.s.P, r = c.rt.r;
+    int id = -1;
+    float own = 0.f;
+    if (tid < P) {
+        id = c.s.dense ? 0 : c.rt.ids[tid];
+        own = c.resp ? c.resp[tid] : 1.f;
+        if (id >= c.s.K) {
+            if (blockIdx.x == 0) set_error(c.err, GMM_ERR_RANGE);
+            id = -1;
+        }
+        if (id < 0) id = -1;
+    }
+    if (P <= 32) {   // one warp, no barriers on the way
+        if (warp == 0) {
+            const unsigned same = __match_any_sync(0xffffffffu, id);
+            // this pair's point's entries, before it and from it on
+            const int p0 = lane / r * r;
+            const unsigned point = (r < 32 ? (1u << r) - 1 : 0xffffffffu) << p0;
+            const bool repeat = ONCE && (same & point & ((1u << lane) - 1));
+            float weight = own;
+            for (int i = 1; i < r; ++i) {
+                const float w = __shfl_down_sync(0xffffffffu, own, i);
+                if (ONCE && lane + i < p0 + r && (same >> (lane + i) & 1)) weight += w;
+            }
+            const unsigned entries = __ballot_sync(0xffffffffu, id >= 0 && !repeat);
+            const unsigned mine = same & entries;
+            const int rank = __popc(mine & ((1u << lane) - 1)), count = __popc(mine);
+            const bool entry = entries >> lane & 1, lead = entry && rank == 0;
+            const unsigned leads = __ballot_sync(0xffffffffu, lead);
+            int x = lead ? count : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += y;
+            }
+            // (a lead's first entry, for the others of its expert)
+            const int e0 = __shfl_sync(0xffffffffu, x - (lead ? count : 0),
+                                       mine ? __ffs(mine) - 1 : lane);
+            if (lead) L.seg[__popc(leads & ((1u << lane) - 1))] = make_int2(id, e0 | count << 16);
+            if (entry) {
+                L.pair[e0 + rank] = (int16_t)lane;
+                L.weight[e0 + rank] = weight;
+            }
+            L.ids[lane] = id;
+            if (lane == 0) L.segs = __popc(leads);
+        }
+        __syncthreads();
+        return;
+    }
+    if (tid < kPairs) {
+        L.ids[tid] = id;
+        L.weight[tid] = own;
+    }
+    __syncthreads();
+    float weight = 0.f;
+    if (id >= 0) {
+        const int p0 = tid / r * r;
+        for (int q = p0; q < p0 + r; ++q) {
+            const bool same = L.ids[q] == id;
+            if (ONCE && same && q < tid) id = -1;
+            if (same && (ONCE ? q >= tid : q == tid)) weight += L.weight[q];
+        }
+    }
+    __syncthreads();
+    if (tid < kPairs) L.ids[tid] = id;
+    __syncthreads();
+    int first = kPairs, rank = 0, count = 0;
+    if (id >= 0) {
+        const int4 *all = reinterpret_cast<const int4 *>(L.ids);
+#pragma unroll 4
+        for (int q = 0; q < (P + 3) / 4; ++q) {
+            const int4 v = all[q];
+            const int e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const bool same = e[i] == id;
+                const int at = 4 * q + i;
+                count += same;
+                rank += same && at < tid;
+                first = same && at < first ? at : first;
             }
         }
     }
+    // entries and segments before this expert's: a scan over the pairs that
+    // name an expert first
+    const bool lead = id >= 0 && first == tid;
+    const int segs = lead ? (count + kCols - 1) / kCols : 0;
+    const int v = lead ? count | segs << 16 : 0;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (warp < kWarps && lane == 31) L.wsum[warp] = x;
+    __syncthreads();
+    int before = x - v, total = 0;
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += L.wsum[w];
+        total += L.wsum[w];
+    }
+    if (lead) {
+        const int e0 = before & 0xffff, s0 = before >> 16;
+        L.start[tid] = e0;
+        for (int i = 0; i < segs; ++i) {
+            const int n = count - i * kCols < kCols ? count - i * kCols : kCols;
+            L.seg[s0 + i] = make_int2(id, (e0 + i * kCols) | n << 16);
+        }
+    }
+    if (tid == 0) L.segs = total >> 16;
+    __syncthreads();
+    if (id >= 0) {
+        const int at = L.start[first] + rank;
+        L.pair[at] = (int16_t)tid;
+        L.weight[at] = weight;
+    }
+    __syncthreads();
 }
 
 // First weight.  grid (row tiles, pairs); R: 16-row groups of a block (gated:
 // gate rows and up rows); the other warps split the contraction.
 template <typename T, int ACT, bool GATED, int R>
-__global__ void __launch_bounds__(kThreads, 2) few_first_kernel(ExpCall c) {
-    constexpr int KS = kWarps / R, COLS = 32;
-    __shared__ float part[KS][R * 16][COLS + 1];
+__global__ void __launch_bounds__(kThreads, 3) few_first_kernel(ExpCall c) {
+    constexpr int KS = kWarps / R;
+    __shared__ float part[KS][R * 16][kCols + 1];
     __shared__ int list[kPairs];    // pairs of this block's expert
     __shared__ int wcount[kWarps];
     const ExpShape &s = c.s;
@@ -148,42 +303,35 @@ __global__ void __launch_bounds__(kThreads, 2) few_first_kernel(ExpCall c) {
     const T *x = (const T *)c.x, *w = (const T *)c.w1 + (size_t)e * s.first() * s.d;
     const T *b = c.b1 ? (const T *)c.b1 + (size_t)e * s.first() : nullptr;
     const int g = lane >> 2, t = lane & 3, grp = warp % R, ks = warp / R;
-    // this lane's two weight rows
-    const int r0 = GATED ? n0 + g : n0 + grp * 16 + g, r1 = r0 + 8;
+    // this lane's two weight rows, and this warp's slice of the contraction
+    const int r0 = min(GATED ? n0 + g : n0 + grp * 16 + g, width - 1);
+    const int r1 = min(GATED ? n0 + g + 8 : n0 + grp * 16 + g + 8, width - 1);
     const T *base = w + (GATED ? (size_t)grp * width * s.d : 0);
-    const T *w0 = r0 < width ? base + (size_t)r0 * s.d : nullptr;
-    const T *w1 = r1 < width ? base + (size_t)r1 * s.d : nullptr;
+    const T *w0 = base + (size_t)r0 * s.d, *w1 = base + (size_t)r1 * s.d;
     const int chunks = (s.d + 31) / 32;
-    for (int col0 = 0; col0 < total; col0 += COLS) {
+    const int k0 = chunks * ks / KS * 32, k1 = min(chunks * (ks + 1) / KS * 32, s.d);
+    for (int col0 = 0; col0 < total; col0 += kCols) {
+        const int cols = min(total - col0, kCols);
         float acc[4][4];
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+        for (int i = 0; i < 16; ++i) (&acc[0][0])[i] = 0.f;
         const T *xp[4];
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
-            const int at = col0 + n * 8 + g;
-            xp[n] = at < total ? x + c.rt.token(list[at]) * s.d : nullptr;
+            const int at = n * 8 + g;
+            xp[n] = x + c.rt.token(list[col0 + (at < cols ? at : 0)]) * s.d;
         }
-        if (total - col0 <= 8) {
-            float one[1][4] = {{0.f, 0.f, 0.f, 0.f}};
-            const T *const x1[1] = {xp[0]};
-            stream_rows<T, 1, 4>(one, w0, w1, x1, s.d, ks, KS, chunks);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[0][i] = one[0][i];
-        } else {
-            stream_rows<T, 4, 2>(acc, w0, w1, xp, s.d, ks, KS, chunks);
-        }
-        __syncthreads();   // the parts of the columns before are read
+        if (cols <= 8) stream_rows<T, 1, 4>(acc, w0, w1, xp, k0, k1);
+        else stream_rows<T, 4, 1>(acc, w0, w1, xp, k0, k1);
+        if (col0) __syncthreads();   // the parts of the columns before are read
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
+            if (n * 8 >= cols) break;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 part[ks][grp * 16 + g + (i >> 1) * 8][n * 8 + t * 2 + (i & 1)] = acc[n][i];
         }
         __syncthreads();
-        const int cols = total - col0 < COLS ? total - col0 : COLS;
         for (int i = threadIdx.x; i < rows * cols; i += kThreads) {
             const int row = i % rows, col = i / rows, out = n0 + row;
             if (out >= width) continue;
@@ -213,119 +361,71 @@ __global__ void __launch_bounds__(kThreads, 2) few_first_kernel(ExpCall c) {
 
 // Second weight.  grid (16-row tiles x C) in clusters of C blocks; dynamic
 // shared memory: kWarps + 1 sums of [N x 16].
-constexpr int kSecondCols = 32;
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) few_second_kernel(ExpCall c, int C) {
+__global__ void __launch_bounds__(kThreads, 3) few_second_kernel(ExpCall c, int C) {
     extern __shared__ float sums[];
-    __shared__ int expert[kPairs];               // the used experts, in the order of their first pair
-    __shared__ __align__(16) int ids[kPairs];
-    __shared__ float resp[kPairs];
-    __shared__ int wcount[kWarps];
-    __shared__ uint8_t lists[kWarps][kPairs];    // per warp: points of a unit
+    __shared__ __align__(16) Lists L;
     const ExpShape &s = c.s;
-    const int P = (int)s.P, N = (int)s.N, r = c.rt.r, warp = threadIdx.x >> 5;
-    const int lane = threadIdx.x & 31;
+    const int N = (int)s.N, r = c.rt.r, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = blockIdx.x % C, n0 = blockIdx.x / C * 16;
-    const int tid = threadIdx.x;
     float *mine = sums + warp * N * 16, *block = sums + kWarps * N * 16;
+    for (int i = tid; i < kWarps * N * 16; i += kThreads) sums[i] = 0.f;
     // ids and weights do not depend on the first kernel
-    int id = -1;
-    float weight = 0.f;
-    if (tid < P) {
-        id = s.dense ? 0 : c.rt.ids[tid];
-        if (id >= s.K) id = -1;
-        weight = c.resp ? c.resp[tid] : 1.f;
+    make_lists<true>(c, L);
+    // this warp's part of the segments' 32-index chunks, laid end to end
+    const int per = (s.h + 31) / 32, total = L.segs * per;
+    const int w = rank * kWarps + warp, warps = C * kWarps;
+    const int beg = (int)((int64_t)total * w / warps), end = (int)((int64_t)total * (w + 1) / warps);
+    // its weights start for L2 while the first kernel ends
+    for (int i = beg; i < end;) {
+        const int sg = i / per, stop = min(end, (sg + 1) * per), row = lane & 15;
+        const int k1 = min((stop - sg * per) * 32, s.h);
+        const T *p = (const T *)c.w2 + ((size_t)L.seg[sg].x * s.o + min(n0 + row, s.o - 1)) * s.h;
+        for (int k = (i - sg * per) * 32 + (lane >> 4) * 64; k < k1; k += 128)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(p + k));
+        i = stop;
     }
-    ids[tid] = id;
-    resp[tid] = weight;
-    for (int i = lane; i < N * 16; i += 32) mine[i] = 0.f;
-    __syncthreads();
-    bool lead = id >= 0;
-    const int4 *all = reinterpret_cast<const int4 *>(ids);
-#pragma unroll 8
-    for (int q = 0; q <= (tid | 31) / 4; ++q) {   // the same trip count for a warp
-        const int4 v = all[q];
-        lead = lead && !((v.x == id && 4 * q < tid) || (v.y == id && 4 * q + 1 < tid) ||
-                         (v.z == id && 4 * q + 2 < tid) || (v.w == id && 4 * q + 3 < tid));
-    }
-    const unsigned votes = __ballot_sync(0xffffffffu, lead);
-    if (lane == 0) wcount[warp] = __popc(votes);
-    __syncthreads();
-    int at = __popc(votes & ((1u << lane) - 1)), E = 0;
-    for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) at += wcount[w];
-        E += wcount[w];
-    }
-    if (lead) expert[at] = id;
-    __syncthreads();
-    // slices of h per expert: as many as the cluster's warps can take at
-    // once, of 128 indices at least
-    const int warps = kWarps * C, chunks = (s.h + 31) / 32;
-    int KS = E > 0 ? warps / E : 1;
-    if (KS > (chunks + 3) / 4) KS = (chunks + 3) / 4;
-    if (KS < 1) KS = 1;
     const int g = lane >> 2, t = lane & 3;
-    const T *hid = (const T *)c.hid;
-    uint8_t *list = lists[warp];
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    for (int unit = warp * C + rank; unit < E * KS; unit += warps) {
-        const int i = unit / KS, ks = unit - i * KS, e = expert[i];
-        // the expert's points; one that lists it twice once, with both weights
-        int total = 0;
-        for (int p0 = 0; p0 < P; p0 += 32) {
-            const int p = p0 + lane;
-            bool in = p < P && ids[p] == e;
-            if (in)
-                for (int q = p / r * r; q < p; ++q) in = in && ids[q] != e;
-            const unsigned v = __ballot_sync(0xffffffffu, in);
-            if (in) list[total + __popc(v & ((1u << lane) - 1))] = (uint8_t)p;
-            total += __popc(v);
+    for (int i = beg; i < end;) {
+        const int sg = i / per, stop = min(end, (sg + 1) * per);
+        const int k0 = (i - sg * per) * 32, k1 = min((stop - sg * per) * 32, s.h);
+        const int2 seg = L.seg[sg];
+        const int e0 = seg.y & 0xffff, cnt = seg.y >> 16;
+        const T *wr = (const T *)c.w2 + (size_t)seg.x * s.o * s.h;
+        const T *w0 = wr + (size_t)min(n0 + g, s.o - 1) * s.h;
+        const T *w1 = wr + (size_t)min(n0 + g + 8, s.o - 1) * s.h;
+        const T *xp[4];
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            const int at = n * 8 + g;
+            xp[n] = (const T *)c.hid + (size_t)L.pair[e0 + (at < cnt ? at : 0)] * s.h;
+        }
+        float acc[4][4];
+#pragma unroll
+        for (int n = 0; n < 16; ++n) (&acc[0][0])[n] = 0.f;
+        if (cnt <= 8) stream_rows<T, 1, 4>(acc, w0, w1, xp, k0, k1);
+        else stream_rows<T, 4, 1>(acc, w0, w1, xp, k0, k1);
+        // to the points' sums: no two lanes have a point and a row in common
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            if (n * 8 >= cnt) break;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int at = n * 8 + t * 2 + (j & 1);
+                if (at < cnt)
+                    mine[(L.pair[e0 + at] / r) * 16 + g + (j >> 1) * 8] +=
+                        L.weight[e0 + at] * acc[n][j];
+            }
         }
         __syncwarp();
-        const T *w = (const T *)c.w2 + (size_t)e * s.o * s.h;
-        const T *w0 = n0 + g < s.o ? w + (size_t)(n0 + g) * s.h : nullptr;
-        const T *w1 = n0 + g + 8 < s.o ? w + (size_t)(n0 + g + 8) * s.h : nullptr;
-        for (int col0 = 0; col0 < total; col0 += kSecondCols) {
-            float acc[4][4];
-#pragma unroll
-            for (int n = 0; n < 4; ++n)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) acc[n][k] = 0.f;
-            const T *xp[4];
-#pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                const int l = col0 + n * 8 + g;
-                xp[n] = l < total ? hid + (size_t)list[l] * s.h : nullptr;
-            }
-            if (total - col0 <= 8) {
-                float one[1][4] = {{0.f, 0.f, 0.f, 0.f}};
-                const T *const x1[1] = {xp[0]};
-                stream_rows<T, 1, 4>(one, w0, w1, x1, s.h, ks, KS, chunks);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) acc[0][k] = one[0][k];
-            } else {
-                stream_rows<T, 4, 2>(acc, w0, w1, xp, s.h, ks, KS, chunks);
-            }
-#pragma unroll
-            for (int n = 0; n < 4; ++n)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int l = col0 + n * 8 + t * 2 + (k & 1);
-                    if (l >= total) continue;
-                    const int p = list[l], tok = p / r;
-                    float gw = 0.f;
-                    for (int q = p; q < (tok + 1) * r; ++q)
-                        if (ids[q] == e) gw += resp[q];
-                    mine[tok * 16 + g + (k >> 1) * 8] += gw * acc[n][k];
-                }
-        }
-        __syncwarp();
+        i = stop;
     }
     __syncthreads();
     for (int i = tid; i < N * 16; i += kThreads) {
         float v = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) v += sums[w * N * 16 + i];
+        for (int k = 0; k < kWarps; ++k) v += sums[k * N * 16 + i];
         block[i] = v;
     }
     cluster_sync_all();
@@ -339,9 +439,12 @@ __global__ void __launch_bounds__(kThreads, 2) few_second_kernel(ExpCall c, int 
             v += x;
         }
         if (c.b2)
-            for (int q = tok * r; q < (tok + 1) * r; ++q)
-                if (ids[q] >= 0)
-                    v = fmaf(resp[q], value_at((const T *)c.b2 + (size_t)ids[q] * s.o + out), v);
+            for (int q = tok * r; q < (tok + 1) * r; ++q) {
+                const int id = s.dense ? 0 : c.rt.ids[q];
+                if (id >= 0 && id < s.K)
+                    v = fmaf(c.resp ? c.resp[q] : 1.f,
+                             value_at((const T *)c.b2 + (size_t)id * s.o + out), v);
+            }
         const size_t y = (size_t)tok * s.o + out;
         if (c.res) v += to_float(((const T *)c.res)[y]);
         ((T *)c.y)[y] = from_float<T>(v);
@@ -360,9 +463,9 @@ cudaError_t launch_first(const ExpCall &c, cudaStream_t st) {
 
 template <typename T> cudaError_t launch_second(const ExpCall &c, cudaStream_t st) {
     const int tiles = (c.s.o + 15) / 16;
-    // about four blocks an SM
+    // one wave at three blocks an SM
     int C = 8;
-    while (C > 1 && tiles * C > 4 * 148) C /= 2;
+    while (C > 1 && tiles * C > 3 * 148) C /= 2;
     const size_t smem = (size_t)(kWarps + 1) * c.s.N * 16 * sizeof(float);
     cudaError_t e = cudaFuncSetAttribute(few_second_kernel<T>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);

@@ -24,8 +24,7 @@
 // is transposed.
 #include "experts.h"
 #include "tc_ptx.cuh"
-
-#include <cuda.h>
+#include "tensor_map.h"
 
 namespace gmmb {
 namespace {
@@ -549,55 +548,13 @@ __global__ void __launch_bounds__(kThreads, 1) exp_tc_kernel(const __grid_consta
 }
 
 // ------------------------------------------------------------- host side
-using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                              const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                              const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeFn encode_fn() {
-    static const EncodeFn fn = [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
-                                             cudaEnableDefault, &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            p = nullptr;
-        return (EncodeFn)p;
-    }();
-    return fn;
-}
-
-struct Maps {
-    gmm_dtype dt;
-    bool ok = true;
-    // [planes x] rows x cols, boxes of 64 columns x box_rows
-    void make(CUtensorMap *m, const void *base, int64_t cols, int64_t rows, int64_t planes,
-              int box_rows) {
-        const EncodeFn fn = encode_fn();
-        if (!fn) {
-            ok = false;
-            return;
-        }
-        const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)planes};
-        const cuuint64_t strides[2] = {(cuuint64_t)cols * 2, (cuuint64_t)cols * rows * 2};
-        const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
-        const cuuint32_t one[3] = {1, 1, 1};
-        ok = ok && fn(m, dt == GMM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                        : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                      planes ? 3 : 2, const_cast<void *>(base), dims, strides, box, one,
-                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-    }
-};
-
 template <typename T, int KIND, int ACT, bool GATED, int CG>
 cudaError_t launch_kind(const ExpCall &c, cudaStream_t st) {
     using C = Cfg<KIND, GATED, CG>;
     const ExpShape &s = c.s;
     Args a;
     a.c = c;
-    Maps maps{s.dt};
+    TensorMaps maps{s.dt};
     int width = 0, mrows = 0;
     switch (KIND) {
         case kFirst:
