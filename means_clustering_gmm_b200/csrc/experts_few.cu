@@ -58,15 +58,6 @@ __device__ __forceinline__ void mma16<__nv_bfloat16>(float (&d)[4], const uint32
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// 16 bytes of weights, read once: not kept in L1.
-__device__ __forceinline__ uint4 stream16(const void *p) {
-    uint4 v;
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
-}
-
 // acc[nt] += 16 weight rows x 8 points over the contraction indices [k0, k1)
 // (k0 a multiple of 32).  w0 / w1: rows g and g + 8; x[nt]: the row of point
 // 8 nt + g.  All are rows that exist (a lane without one of its own repeats
@@ -91,8 +82,8 @@ __device__ __forceinline__ void stream_rows(float (&acc)[4][4], const T *w0, con
         uint4 a0[U], a1[U], b[U][NT];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            a0[u] = stream16(w0 + k + u * 32);
-            a1[u] = stream16(w1 + k + u * 32);
+            a0[u] = *reinterpret_cast<const uint4 *>(w0 + k + u * 32);
+            a1[u] = *reinterpret_cast<const uint4 *>(w1 + k + u * 32);
 #pragma unroll
             for (int n = 0; n < NT; ++n)
                 b[u][n] = *reinterpret_cast<const uint4 *>(x[n] + k + u * 32);
@@ -104,8 +95,8 @@ __device__ __forceinline__ void stream_rows(float (&acc)[4][4], const T *w0, con
         uint4 a0 = make_uint4(0u, 0u, 0u, 0u), a1 = a0, b[NT];
         const bool in = k < k1;
         if (in) {
-            a0 = stream16(w0 + k);
-            a1 = stream16(w1 + k);
+            a0 = *reinterpret_cast<const uint4 *>(w0 + k);
+            a1 = *reinterpret_cast<const uint4 *>(w1 + k);
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -256,7 +247,7 @@ __device__ __forceinline__ void make_lists(const ExpCall &c, Lists &L) {
 // First weight.  grid (row tiles, pairs); R: 16-row groups of a block (gated:
 // gate rows and up rows); the other warps split the contraction.
 template <typename T, int ACT, bool GATED, int R>
-__global__ void __launch_bounds__(kThreads, 3) few_first_kernel(ExpCall c) {
+__global__ void __launch_bounds__(kThreads, 4) few_first_kernel(ExpCall c) {
     constexpr int KS = kWarps / R;
     __shared__ float part[KS][R * 16][kCols + 1];
     __shared__ int list[kPairs];    // pairs of this block's expert
@@ -315,14 +306,16 @@ __global__ void __launch_bounds__(kThreads, 3) few_first_kernel(ExpCall c) {
         float acc[4][4];
 #pragma unroll
         for (int i = 0; i < 16; ++i) (&acc[0][0])[i] = 0.f;
-        const T *xp[4];
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            const int at = n * 8 + g;
-            xp[n] = x + c.rt.token(list[col0 + (at < cols ? at : 0)]) * s.d;
+        auto point = [&](int at) {
+            return x + c.rt.token(list[col0 + (at < cols ? at : 0)]) * s.d;
+        };
+        if (cols <= 8) {
+            const T *const xp[4] = {point(g)};
+            stream_rows<T, 1, 4>(acc, w0, w1, xp, k0, k1);
+        } else {
+            const T *const xp[4] = {point(g), point(g + 8), point(g + 16), point(g + 24)};
+            stream_rows<T, 4, 1>(acc, w0, w1, xp, k0, k1);
         }
-        if (cols <= 8) stream_rows<T, 1, 4>(acc, w0, w1, xp, k0, k1);
-        else stream_rows<T, 4, 1>(acc, w0, w1, xp, k0, k1);
         if (col0) __syncthreads();   // the parts of the columns before are read
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
