@@ -94,6 +94,8 @@ class GmmError(RuntimeError):
 
 def load() -> ctypes.CDLL:
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):

@@ -23,7 +23,7 @@ import torch
 
 from . import _lib
 from ._lib import GMM_FLAG_NONE, ExpertShape, check
-from .api import _DT, Workspace, _ptr
+from .api import _DT, Workspace
 
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3}
 
@@ -31,13 +31,24 @@ __all__ = ["expert_linear", "expert_linear_backward", "expert_mlp", "expert_mlp_
            "expert_path", "expert_workspace_size"]
 
 
-def _shape(N, d, h, o, K, r, dtype, activation="none", gated=False) -> ExpertShape:
-    if activation not in ACTIVATIONS:
-        raise ValueError(f"activation: expected one of {sorted(ACTIVATIONS)}, got {activation!r}")
-    if dtype not in _DT:
-        raise ValueError("dtype must be float32, bfloat16 or float16")
-    return ExpertShape(N=N, d=d, h=h, o=o, K=K, r=r, dtype=_DT[dtype],
-                       activation=ACTIVATIONS[activation], gated=int(bool(gated)))
+_shapes = {}   # ExpertShape (and its pointer) by the values it holds
+
+
+def _shape(N, d, h, o, K, r, dtype, activation="none", gated=False):
+    key = (N, d, h, o, K, r, dtype, activation, gated)
+    p = _shapes.get(key)
+    if p is None:
+        if activation not in ACTIVATIONS:
+            raise ValueError(
+                f"activation: expected one of {sorted(ACTIVATIONS)}, got {activation!r}")
+        if dtype not in _DT:
+            raise ValueError("dtype must be float32, bfloat16 or float16")
+        if len(_shapes) >= 4096:
+            _shapes.clear()
+        p = _shapes[key] = ctypes.pointer(ExpertShape(
+            N=N, d=d, h=h, o=o, K=K, r=r, dtype=_DT[dtype], activation=ACTIVATIONS[activation],
+            gated=int(bool(gated))))
+    return p
 
 
 def expert_workspace_size(N: int, d: int, h: int, o: int, K: int, r: int, dtype=torch.bfloat16,
@@ -46,7 +57,7 @@ def expert_workspace_size(N: int, d: int, h: int, o: int, K: int, r: int, dtype=
     """Bytes of workspace of expert_linear (h = 0) or expert_mlp, 0 for invalid
     sizes; r = 0 is the dense form."""
     return int(_lib.load().gmm_expert_workspace_size(
-        ctypes.byref(_shape(N, d, h, o, K, r, dtype, gated=gated)), int(backward), int(flags)))
+        _shape(N, d, h, o, K, r, dtype, gated=gated), int(backward), int(flags)))
 
 
 def expert_path(N: int, d: int, h: int, o: int, K: int, r: int, dtype=torch.bfloat16,
@@ -54,14 +65,14 @@ def expert_path(N: int, d: int, h: int, o: int, K: int, r: int, dtype=torch.bflo
     """Which kernels a call of these sizes runs: 0 CUDA cores, 1 the form for
     few points, 2 tensor cores (gmm_expert_path)."""
     path = int(_lib.load().gmm_expert_path(
-        ctypes.byref(_shape(N, d, h, o, K, r, dtype, gated=gated)), int(backward), int(flags)))
+        _shape(N, d, h, o, K, r, dtype, gated=gated), int(backward), int(flags)))
     if path < 0:
         raise ValueError("invalid problem size")
     return path
 
 
 def _tensor(t, name, dtype, shape, dev):
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or tuple(t.shape) != tuple(shape) or \
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or \
             t.device != dev or not t.is_contiguous():
         got = f"{t.dtype} {tuple(t.shape)} on {t.device}" if isinstance(t, torch.Tensor) else t
         raise ValueError(f"{name}: expected contiguous {dtype} {tuple(shape)} on {dev}, got {got}")
@@ -73,27 +84,31 @@ def _tensor(t, name, dtype, shape, dev):
 
 class _Call:
     """The arguments the four calls share, checked, with the device and the
-    stream they run on."""
+    stream they run on.  As a context it makes both current where they are
+    not, so that outputs belong to the stream that writes them."""
+
+    __slots__ = ("dev", "dtype", "N", "d", "h", "o", "K", "r", "first", "shape", "ws", "stream",
+                 "guard")
 
     def __init__(self, X, ids, resp, W1, W2, ws, activation, gated, stream):
-        if not isinstance(X, torch.Tensor) or X.dim() != 2 or X.dtype not in _DT or \
-                not X.is_cuda or not X.is_contiguous():
+        if not isinstance(X, torch.Tensor) or X.dim() != 2 or X.dtype not in _DT or not X.is_cuda:
             raise ValueError("X must be a contiguous cuda float32/bfloat16/float16 [N, d] tensor")
-        self.dev, self.dtype = X.device, X.dtype
-        _tensor(X, "X", X.dtype, X.shape, X.device)
-        N, d = X.shape
-        weights = (W1,) if W2 is None else (W1, W2)
-        if any(not isinstance(w, torch.Tensor) or w.dim() != 3 for w in weights):
-            raise ValueError("weights must be [K, out, in] tensors")
-        K, first = W1.shape[0], W1.shape[1]
+        dev, dtype, size = X.device, X.dtype, X.shape
+        _tensor(X, "X", dtype, size, dev)
+        N, d = size
+        for w in (W1,) if W2 is None else (W1, W2):
+            if not isinstance(w, torch.Tensor) or w.dim() != 3:
+                raise ValueError("weights must be [K, out, in] tensors")
+        K, first, _ = W1.shape
         if W2 is None:
             h, o = 0, first
+            _tensor(W1, "W", dtype, (K, first, d), dev)
         else:
             if gated and first % 2:
                 raise ValueError("gated: W1 must have 2h rows")
             h, o = first // 2 if gated else first, W2.shape[1]
-            _tensor(W2, "W2", X.dtype, (K, o, h), X.device)
-        _tensor(W1, "W" if W2 is None else "W1", X.dtype, (K, first, d), X.device)
+            _tensor(W1, "W1", dtype, (K, first, d), dev)
+            _tensor(W2, "W2", dtype, (K, o, h), dev)
         if ids is None:
             if resp is not None:
                 raise ValueError("resp needs ids")
@@ -104,39 +119,52 @@ class _Call:
             if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
                 raise ValueError("ids must be an int32 [N, r] tensor")
             r = ids.shape[1]
-            _tensor(ids, "ids", torch.int32, (N, r), X.device)
+            _tensor(ids, "ids", torch.int32, (N, r), dev)
             if not 1 <= r <= 8:
                 raise ValueError(f"r must be 1..8, got {r}")
             if resp is not None:
-                _tensor(resp, "resp", torch.float32, (N, r), X.device)
-        if not isinstance(ws, Workspace) or ws.view.device != X.device:
-            raise ValueError(f"ws must be a Workspace on {X.device}")
+                _tensor(resp, "resp", torch.float32, (N, r), dev)
+        if not isinstance(ws, Workspace) or ws.view.device != dev:
+            raise ValueError(f"ws must be a Workspace on {dev}")
+        self.dev, self.dtype, self.ws = dev, dtype, ws
         self.N, self.d, self.h, self.o, self.K, self.r, self.first = N, d, h, o, K, r, first
-        self.shape = _shape(N, d, h, o, K, r, X.dtype, activation, gated)
-        self.ws = ws
-        self.stream = torch.cuda.current_stream(X.device) if stream is None else stream
-        if self.stream.device != X.device:
-            raise ValueError(f"stream is on {self.stream.device}, X on {X.device}")
+        self.shape = _shape(N, d, h, o, K, r, dtype, activation, bool(gated))
+        self.guard = None
+        if stream is not None:
+            if stream.device != dev:
+                raise ValueError(f"stream is on {stream.device}, X on {dev}")
+            self.guard = torch.cuda.stream(stream)
+        elif torch.cuda.current_device() != dev.index:
+            self.guard = torch.cuda.device(dev)
 
     def bias(self, b, name, width):
-        return None if b is None else _tensor(b, name, self.dtype, (self.K, width), self.dev)
+        if b is not None:
+            _tensor(b, name, self.dtype, (self.K, width), self.dev)
 
     def rows(self, t, name, width):
         return _tensor(t, name, self.dtype, (self.N, width), self.dev)
 
-    def new(self, like):
-        return None if like is None else torch.empty_like(like)
+    def out(self, t, width):
+        return torch.empty((self.N, width), dtype=self.dtype, device=self.dev) if t is None \
+            else self.rows(t, "out", width)
 
-    def run(self, fn, *args):
-        ptrs = [_ptr(a) for a in args]
-        check(fn, getattr(_lib.load(), fn)(ctypes.byref(self.shape), *ptrs, self.ws.ptr,
-                                           self.ws.nbytes, self.flags, self.stream.cuda_stream))
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        # (torch.cuda.current_stream(), without building a Stream)
+        self.stream = torch._C._cuda_getCurrentRawStream(self.dev.index)
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+    def run(self, name, fn, flags, *args):
+        check(name, fn(self.shape, *[None if t is None else t.data_ptr() for t in args],
+                       self.ws.ptr, self.ws.nbytes, int(flags), self.stream))
 
 
-def _on(call):
-    """The call's device and stream made current, so that outputs belong to
-    the stream that writes them."""
-    return torch.cuda.stream(call.stream)
+def _like(t):
+    return None if t is None else torch.empty_like(t)
 
 
 def expert_linear(X, ids, resp, W, b, ws: Workspace, activation: str = "none", residual=None,
@@ -147,14 +175,13 @@ def expert_linear(X, ids, resp, W, b, ws: Workspace, activation: str = "none", r
     or None.  Returns [N, o], written to ``out`` when given (which may be the
     residual)."""
     c = _Call(X, ids, resp, W, None, ws, activation, False, stream)
-    c.flags = int(flags)
     c.bias(b, "b", c.o)
     if residual is not None:
         c.rows(residual, "residual", c.o)
-    with _on(c):
-        Y = torch.empty((c.N, c.o), dtype=c.dtype, device=c.dev) if out is None else \
-            c.rows(out, "out", c.o)
-        c.run("gmm_expert_linear", X, ids, resp, W, b, residual, Y)
+    with c:
+        Y = c.out(out, c.o)
+        c.run("gmm_expert_linear", _lib.load().gmm_expert_linear, flags, X, ids, resp, W, b,
+              residual, Y)
     return Y
 
 
@@ -163,12 +190,11 @@ def expert_linear_backward(dY, X, ids, resp, W, b, ws: Workspace, activation: st
     """Gradients of expert_linear's inputs for dY [N, o]: (dX, dW, db or None,
     dresp or None).  The residual's gradient is dY itself."""
     c = _Call(X, ids, resp, W, None, ws, activation, False, stream)
-    c.flags = int(flags)
     c.bias(b, "b", c.o)
     c.rows(dY, "dY", c.o)
-    with _on(c):
-        dX, dW, db, dresp = (c.new(t) for t in (X, W, b, resp))
-        c.run("gmm_expert_linear_backward", dY, X, ids, resp, W, b, dX, dW, db, dresp)
+    with c:
+        dX, dW, db, dresp = _like(X), _like(W), _like(b), _like(resp)
+        c.run("gmm_expert_linear_backward", _lib.load().gmm_expert_linear_backward, flags, dY, X, ids, resp, W, b, dX, dW, db, dresp)
     return dX, dW, db, dresp
 
 
@@ -180,15 +206,14 @@ def expert_mlp(X, ids, resp, W1, b1, W2, b2, ws: Workspace, activation: str = "s
     W1 [K, h or 2h, d], b1 [K, h or 2h] or None, W2 [K, o, h], b2 [K, o] or
     None; the rest as expert_linear."""
     c = _Call(X, ids, resp, W1, W2, ws, activation, gated, stream)
-    c.flags = int(flags)
     c.bias(b1, "b1", c.first)
     c.bias(b2, "b2", c.o)
     if residual is not None:
         c.rows(residual, "residual", c.o)
-    with _on(c):
-        Y = torch.empty((c.N, c.o), dtype=c.dtype, device=c.dev) if out is None else \
-            c.rows(out, "out", c.o)
-        c.run("gmm_expert_mlp", X, ids, resp, W1, b1, W2, b2, residual, Y)
+    with c:
+        Y = c.out(out, c.o)
+        c.run("gmm_expert_mlp", _lib.load().gmm_expert_mlp, flags, X, ids, resp, W1, b1, W2, b2,
+              residual, Y)
     return Y
 
 
@@ -198,12 +223,11 @@ def expert_mlp_backward(dY, X, ids, resp, W1, b1, W2, b2, ws: Workspace, activat
     dW2, db2 or None, dresp or None).  The residual's gradient is dY itself.
     Needs a workspace made with ``backward=True``."""
     c = _Call(X, ids, resp, W1, W2, ws, activation, gated, stream)
-    c.flags = int(flags)
     c.bias(b1, "b1", c.first)
     c.bias(b2, "b2", c.o)
     c.rows(dY, "dY", c.o)
-    with _on(c):
-        dX, dW1, db1, dW2, db2, dresp = (c.new(t) for t in (X, W1, b1, W2, b2, resp))
-        c.run("gmm_expert_mlp_backward", dY, X, ids, resp, W1, b1, W2, b2, dX, dW1, db1, dW2, db2,
-              dresp)
+    with c:
+        dX, dW1, db1, dW2, db2, dresp = (_like(t) for t in (X, W1, b1, W2, b2, resp))
+        c.run("gmm_expert_mlp_backward", _lib.load().gmm_expert_mlp_backward, flags, dY, X, ids,
+              resp, W1, b1, W2, b2, dX, dW1, db1, dW2, db2, dresp)
     return dX, dW1, db1, dW2, db2, dresp
