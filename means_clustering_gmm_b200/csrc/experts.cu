@@ -83,7 +83,7 @@ Layout layout_of(const ExpShape &p, bool backward, int path) {
     take(L.da, backward ? (size_t)L.max_rows * p.first() * L.esize : 0);
     const bool sorted = path == 2 && !p.dense;
     take(L.xrows, sorted ? (size_t)L.max_rows * p.d * 2 : 0);
-    take(L.dyrows, sorted && backward ? (size_t)L.max_rows * p.o * 2 : 0);
+    take(L.dyrows, sorted && backward && p.mlp ? (size_t)L.max_rows * p.o * 2 : 0);
     const int wide = !backward ? p.o : (p.d > p.o ? p.d : p.o);
     take(L.slots, p.direct() ? 0 : (size_t)p.P * wide * 4);
     take(L.rpart, backward ? (size_t)L.max_rows * L.nrpart * 4 : 0);

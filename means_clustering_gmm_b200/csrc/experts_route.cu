@@ -27,13 +27,18 @@ exp_hist_kernel(ExpRoute rt, int *err) {
     const int64_t chunk = (int64_t)blockIdx.x * 4 + warp;
     const int64_t p0 = chunk * kChunkPairs;
     if (p0 >= rt.P) return;
+    int key[kChunkPairs / 32];
+#pragma unroll
+    for (int u = 0; u < kChunkPairs / 32; ++u) {
+        const int64_t p = p0 + u * 32 + lane;
+        key[u] = p < rt.P ? pair_key(rt.ids, p, rt.K, err) : -1;
+    }
     for (int e = lane; e < KK; e += 32) row[e] = 0;
     __syncwarp();
-    for (int i = 0; i < kChunkPairs; i += 32) {
-        const int64_t p = p0 + i + lane;
-        const int key = p < rt.P ? pair_key(rt.ids, p, rt.K, err) : -1;
-        const unsigned same = __match_any_sync(0xffffffffu, key);
-        if (key >= 0 && lane == __ffs(same) - 1) row[key] += __popc(same);
+#pragma unroll
+    for (int u = 0; u < kChunkPairs / 32; ++u) {
+        const unsigned same = __match_any_sync(0xffffffffu, key[u]);
+        if (key[u] >= 0 && lane == __ffs(same) - 1) row[key[u]] += __popc(same);
         __syncwarp();
     }
     for (int e = lane; e < KK; e += 32) rt.hist[chunk * KK + e] = row[e];
@@ -221,20 +226,24 @@ exp_scatter_kernel(ExpRoute rt) {
     const int64_t chunk = (int64_t)blockIdx.x * 4 + warp;
     const int64_t p0 = chunk * kChunkPairs;
     if (p0 >= rt.P) return;
+    int key[kChunkPairs / 32];
+#pragma unroll
+    for (int u = 0; u < kChunkPairs / 32; ++u) {
+        const int64_t p = p0 + u * 32 + lane;
+        key[u] = p < rt.P ? pair_key(rt.ids, p, rt.K, nullptr) : -1;
+        if (key[u] == rt.K && rt.r > 1) key[u] = -1;
+    }
     for (int e = lane; e < KK; e += 32) row[e] = rt.seg[e] + rt.hist[chunk * KK + e];
     __syncwarp();
-    for (int i = 0; i < kChunkPairs; i += 32) {
-        const int64_t p = p0 + i + lane;
-        int key = -1;
-        if (p < rt.P) key = pair_key(rt.ids, p, rt.K, nullptr);
-        if (key == rt.K && rt.r > 1) key = -1;
-        const unsigned same = __match_any_sync(0xffffffffu, key);
+#pragma unroll
+    for (int u = 0; u < kChunkPairs / 32; ++u) {
+        const unsigned same = __match_any_sync(0xffffffffu, key[u]);
         const int rank = __popc(same & ((1u << lane) - 1));
-        const int base = key >= 0 ? row[key] : 0;
+        const int base = key[u] >= 0 ? row[key[u]] : 0;
         __syncwarp();
-        if (key >= 0) {
-            rt.row_pair[base + rank] = (int)p;
-            if (rank == 0) row[key] = base + __popc(same);
+        if (key[u] >= 0) {
+            rt.row_pair[base + rank] = (int)(p0 + u * 32 + lane);
+            if (rank == 0) row[key[u]] = base + __popc(same);
         }
         __syncwarp();
     }
@@ -309,7 +318,8 @@ exp_gather_kernel(ExpRoute rt, const uint4 *__restrict__ x, uint4 *__restrict__ 
 
 cudaError_t launch_exp_gather(const ExpCall &c, bool backward, cudaStream_t s) {
     const int64_t want = (c.max_rows + 7) / 8;
-    const dim3 grid((unsigned)(want < 148 * 8 ? want : 148 * 8), backward ? 2 : 1);
+    // (the linear form's gradients read dY through the pairs instead)
+    const dim3 grid((unsigned)(want < 148 * 8 ? want : 148 * 8), backward && c.s.mlp ? 2 : 1);
     exp_gather_kernel<<<grid, 256, 0, s>>>(c.rt, (const uint4 *)c.x, (uint4 *)c.xrows, c.s.d / 8,
                                            (const uint4 *)c.dy, (uint4 *)c.dyrows, c.s.o / 8);
     note_launches(1);

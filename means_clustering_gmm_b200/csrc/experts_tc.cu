@@ -15,8 +15,10 @@
 //   warp 1       tcgen05.mma, M = 128, N up to 256, fp32 accumulators in
 //                TMEM, two buffers of 256 columns: the epilogue of one tile
 //                runs under the products of the next.
-//   warps 2..9   epilogue, two warps per TMEM lane quadrant, each half of
-//                the tile's columns; a thread owns one row.
+//   warps 2..17  epilogue, four warps per TMEM lane quadrant, each a quarter
+//                of the tile's columns; a thread owns one row and takes 16
+//                columns at a time (eight warps with 32 columns each waited
+//                for their loads half of the time).
 //
 // Operands are used as they lie in memory: a contraction over an array's
 // contiguous axis reads it K-major, one over its rows (the weights in the
@@ -32,7 +34,8 @@ namespace {
 using namespace tc;
 
 constexpr int kSms = 148;
-constexpr int kThreads = 320;
+constexpr int kEpiWarps = 16;
+constexpr int kThreads = 64 + kEpiWarps * 32;
 constexpr int kRowsA = 128;          // rows of a tile (points, or weight rows of dW)
 constexpr int kStepK = 64;           // contraction indices per stage
 constexpr int kBytesA = kRowsA * kStepK * 2;
@@ -59,20 +62,27 @@ enum Kind {
 // (phase 1, two buffers of 128 columns), then the pre-activations (phase 2).
 // Gated, those take the other 256 columns, once: the next tile's phase 1
 // covers the epilogue.  Otherwise they are double-buffered too.
-template <int KIND, bool GATED, int CG> struct Cfg {
+//
+// W: columns of the other kinds' tiles, 128 where the result has no more.
+template <int KIND, bool GATED, int CG, int W> struct Cfg {
     static constexpr bool kGrad = KIND == kDw1 || KIND == kDw2;
     static constexpr bool kTwo = KIND == kDaMlp;
-    static constexpr int NB = kTwo || (KIND == kFirst && GATED) ? 128 : 256;
-    static constexpr int N1 = kTwo ? 128 : 256;
+    static constexpr int NB = kTwo || (KIND == kFirst && GATED) ? 128 : W;
+    static constexpr int N1 = kTwo ? 128 : KIND == kFirst && GATED ? 256 : W;
     static constexpr int N2 = kTwo ? (GATED ? 256 : 128) : 0;
     static constexpr int kB1 = N1 / CG * kStepK * 2, kB2 = N2 / CG * kStepK * 2;
     static constexpr int kBytesB = kB1 > kB2 ? kB1 : kB2;
     static constexpr int kStage = kBytesA + kBytesB;
-    static constexpr int kStages = 192 * 1024 / kStage;
+    static constexpr int kStages = 192 * 1024 / kStage < 8 ? 192 * 1024 / kStage : 8;
+    static constexpr int kPart = NB / 4;   // columns of an epilogue warp
     // what an epilogue warp keeps of its columns' biases (gate and up), fp32
     static constexpr bool kBias = !kGrad && KIND != kDx;
-    static constexpr int kBiasBytes = kBias ? 8 * 2 * 128 * 4 : 0;
+    static constexpr int kBiasBytes = kBias ? kEpiWarps * 2 * 64 * 4 : 0;
     static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + kBiasBytes + 256;
+    // one CTA per tile is for short segments: only the 32-row groups of A
+    // that hold rows are fetched (the products of the others are not used)
+    static constexpr bool kSmallA = CG == 1 && !kGrad;
+    static constexpr int kBoxA = kSmallA ? 32 : kRowsA;
     static constexpr bool kAMn = kGrad;
     static constexpr bool kBMn1 = kGrad || KIND == kDx || kTwo;
     static constexpr int kTileRows = kRowsA * CG;
@@ -104,15 +114,15 @@ struct Job {
     int64_t row0;
 };
 
-template <int KIND, bool GATED, int CG>
+template <int KIND, bool GATED, int CG, int W>
 __device__ __forceinline__ int total_jobs(const Args &a) {
-    return Cfg<KIND, GATED, CG>::kGrad ? a.c.s.K * a.ntm * a.ntn
+    return Cfg<KIND, GATED, CG, W>::kGrad ? a.c.s.K * a.ntm * a.ntn
                                        : a.c.rt.tiles(CG * kRowsA) * a.ntn;
 }
 
-template <int KIND, bool GATED, int CG>
+template <int KIND, bool GATED, int CG, int W>
 __device__ __forceinline__ Job job_of(const Args &a, int idx, int rank) {
-    using C = Cfg<KIND, GATED, CG>;
+    using C = Cfg<KIND, GATED, CG, W>;
     Job j;
     const ExpShape &s = a.c.s;
     const int t = idx / a.ntn;
@@ -161,21 +171,41 @@ template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float x, fl
     const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
     return *reinterpret_cast<const uint32_t *>(&h);
 }
+__device__ __forceinline__ void store32(void *p, const uint32_t (&w)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
+                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+// Sixteen consecutive results (the first eight where `both` is false).
+// wide: 32-byte aligned, one whole sector in one store.
 template <typename T>
-__device__ __forceinline__ void store8(T *p, const float (&v)[8]) {
-    *reinterpret_cast<uint4 *>(p) = make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]),
-                                               pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7]));
+__device__ __forceinline__ void store16(T *p, const float (&v)[16], bool both, bool wide) {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = pack2<T>(v[2 * i], v[2 * i + 1]);
+    if (wide) {
+        store32(p, w);
+        return;
+    }
+    uint4 *o = reinterpret_cast<uint4 *>(p);
+    o[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    if (both) o[1] = make_uint4(w[4], w[5], w[6], w[7]);
+}
+__device__ __forceinline__ void store16(float *p, const float (&v)[16], bool both, bool) {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(v[i]);
+    store32(p, w);
+    if (both) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(v[8 + i]);
+        store32(p + 8, w);
+    }
 }
 
-__device__ __forceinline__ void store8(float *p, const float (&v)[8]) {
-    float4 *o = reinterpret_cast<float4 *>(p);
-    o[0] = make_float4(v[0], v[1], v[2], v[3]);
-    o[1] = make_float4(v[4], v[5], v[6], v[7]);
-}
-
-template <typename T, int KIND, int ACT, bool GATED, int CG>
+template <typename T, int KIND, int ACT, bool GATED, int CG, int W>
 __global__ void __launch_bounds__(kThreads, 1) exp_tc_kernel(const __grid_constant__ Args a) {
-    using C = Cfg<KIND, GATED, CG>;
+    using C = Cfg<KIND, GATED, CG, W>;
     extern __shared__ uint8_t raw_smem[];
     uint8_t *sm = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~(uintptr_t)1023);
@@ -198,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1) exp_tc_kernel(const __grid_consta
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars->accfull[i], 1);
-            mbar_init(&bars->accfree[i], 8 * CG);
+            mbar_init(&bars->accfree[i], kEpiWarps * CG);
         }
         mbar_init(&bars->done, 1);
         *abort_flag = 0;
@@ -219,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1) exp_tc_kernel(const __grid_consta
     else __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const int total = total_jobs<KIND, GATED, CG>(a);
+    const int total = total_jobs<KIND, GATED, CG, W>(a);
 
     if (warp == 0) {
         // ================================================ TMA producer
@@ -231,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1) exp_tc_kernel(const __grid_consta
         if (lane == 0) {
             bool ok = true;
             for (int idx = first; idx < total && ok; idx += stride) {
-                const Job j = job_of<KIND, GATED, CG>(a, idx, rank);
+                const Job j = job_of<KIND, GATED, CG, W>(a, idx, rank);
                 const int steps = j.steps1 + j.steps2, row = (int)j.row0;
                 for (int st = 0; st < steps; ++st, ++fill) {
                     const int slot = fill % C::kStages;
@@ -241,8 +271,10 @@ __global__ void __launch_bounds__(kThreads, 1) exp_tc_kernel(const __grid_consta
                     uint8_t *A = sm + (size_t)slot * C::kStage, *B = A + kBytesA;
                     const bool second = C::kTwo && st >= j.steps1;
                     if (rank == 0)
-                        mbar_arrive_expect_tx(&bars->full[slot],
-                                              CG * (kBytesA + (second ? C::kB2 : C::kB1)));
+                        mbar_arrive_expect_tx(
+                            &bars->full[slot],
+                            CG * ((second ? C::kB2 : C::kB1) +
+                                  (C::kSmallA ? (j.valid + 31) / 32 * (kBytesA / 4) : kBytesA)));
                     const uint32_t bar = CG == 2 ? mapa_u32(&bars->full[slot], 0)
                                                  : smem_u32(&bars->full[slot]);
                     auto box2 = [&](uint8_t *dst, const CUtensorMap *m, int x, int y) {
@@ -254,6 +286,14 @@ __global__ void __launch_bounds__(kThreads, 1) exp_tc_kernel(const __grid_consta
                         else tma_g2s_3d(dst, m, x, y, j.expert, &bars->full[slot]);
                     };
                     const int k = (second ? st - j.steps1 : st) * kStepK;
+                    auto rows_a = [&](const CUtensorMap *m) {
+                        if constexpr (C::kSmallA) {
+                            for (int i = 0; i * 32 < j.valid; ++i)
+                                box2(A + i * (kBytesA / 4), m, k, row + i * 32);
+                        } else {
+                            box2(A, m, k, row);
+                        }
+                    };
                     // this CTA's first column of B in a phase of N columns
                     const int n1 = j.col0 + rank * (C::N1 / CG);
                     if constexpr (C::kGrad) {
@@ -264,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1) exp_tc_kernel(const __grid_consta
                         for (int i = 0; i < C::N1 / CG / 64; ++i)
                             box2(B + i * kBlk, &a.b, n1 + i * 64, row + k);
                     } else if (!second) {
-                        box2(A, &a.a, k, row);
+                        rows_a(&a.a);
                         if constexpr (C::kBMn1) {
 #pragma unroll
                             for (int i = 0; i < C::N1 / CG / 64; ++i)
@@ -282,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1) exp_tc_kernel(const __grid_consta
                             box3(B, &a.b, k, n1);
                         }
                     } else {
-                        box2(A, &a.a2, k, row);
+                        rows_a(&a.a2);
                         if constexpr (GATED && CG == 1) {
                             box3(B, &a.b2, k, j.col0);
                             box3(B + C::kB2 / 2, &a.b2, k, j.col0 + s.h);
@@ -332,10 +372,10 @@ __global__ void __launch_bounds__(kThreads, 1) exp_tc_kernel(const __grid_consta
             uint32_t use = 0, tile = 0;
             bool ok = true;
             int idx = first;
-            Job nxt = idx < total ? job_of<KIND, GATED, CG>(a, idx, 0) : Job{};
+            Job nxt = idx < total ? job_of<KIND, GATED, CG, W>(a, idx, 0) : Job{};
             for (; idx < total && ok; idx += stride, ++tile) {
                 const Job j = nxt;
-                if (idx + stride < total) nxt = job_of<KIND, GATED, CG>(a, idx + stride, 0);
+                if (idx + stride < total) nxt = job_of<KIND, GATED, CG, W>(a, idx + stride, 0);
                 const int buf = tile & 1;
                 if (!free_wait(buf, ((tile >> 1) & 1) ^ 1)) break;
                 tc_fence_after();
@@ -375,10 +415,10 @@ __global__ void __launch_bounds__(kThreads, 1) exp_tc_kernel(const __grid_consta
         }
     } else {
         // ================================================ epilogue
-        const int q = warp & 3, hf = (warp - 2) >> 2, m = q * 32 + lane;
+        const int q = warp & 3, pt = (warp - 2) >> 2, m = q * 32 + lane;
         const uint32_t lane_base = (uint32_t)(q * 32) << 16;
-        constexpr int kHalf = C::NB / 2;
-        float *gate_b = bias_sm + (warp - 2) * 256, *up_b = gate_b + 128;
+        constexpr int kPart = C::kPart;
+        float *gate_b = bias_sm + (warp - 2) * 128, *up_b = gate_b + 64;
         // columns of the result, and of the rows that are added or multiplied
         const int width = KIND == kDw2                        ? s.h
                           : KIND == kDw1 || KIND == kDx       ? s.d
@@ -389,10 +429,13 @@ __global__ void __launch_bounds__(kThreads, 1) exp_tc_kernel(const __grid_consta
         const bool with_res = (KIND == kSecond || (KIND == kFirst && !s.mlp)) && s.direct() && c.res;
         const bool with_aux = KIND == kDaLin || with_res;
         const bool aux_vec = KIND == kDaLin || a.vec_res;
+        // (workspace rows are aligned; the caller's arrays may be to 16 bytes)
+        const void *dst = KIND == kDw1 ? c.dw1 : KIND == kDw2 ? c.dw2 : KIND == kDx ? c.dx : c.y;
+        const bool wide = width % 16 == 0 && ((uintptr_t)dst & 31) == 0;
         uint32_t tile = 0;
         for (int idx = first; idx < total; idx += stride, ++tile) {
-            const Job j = job_of<KIND, GATED, CG>(a, idx, rank);
-            const int buf = tile & 1;
+            const Job j = job_of<KIND, GATED, CG, W>(a, idx, rank);
+            const int buf = tile & 1, cw = j.col0 + pt * kPart;   // this warp's first column
             const bool none = !C::kGrad && j.expert >= s.K;
             const bool valid = m < j.valid;
             const int64_t row = j.row0 + m;
@@ -407,25 +450,23 @@ __global__ void __launch_bounds__(kThreads, 1) exp_tc_kernel(const __grid_consta
                 const T *b = (const T *)(KIND == kSecond ? c.b2 : c.b1);
                 if (b && !none) b += (size_t)j.expert * (KIND == kSecond ? s.o : s.first());
 #pragma unroll
-                for (int i = lane; i < kHalf; i += 32) {
-                    const int col = j.col0 + hf * kHalf + i;
-                    const bool in = b && !none && col < width;
-                    gate_b[i] = in ? to_float(b[col]) : 0.f;
-                    if (GATED) up_b[i] = in ? to_float(b[width + col]) : 0.f;
+                for (int i = lane; i < kPart; i += 32) {
+                    const bool in = b && !none && cw + i < width;
+                    gate_b[i] = in ? to_float(b[cw + i]) : 0.f;
+                    if (GATED) up_b[i] = in ? to_float(b[width + cw + i]) : 0.f;
                 }
             }
-            // the other array's row, 32 columns ahead of their use
+            // the other array's row, 16 columns ahead of their use
             const T *aux = (const T *)(KIND == kDaLin ? c.dy : c.res) + tok * width;
-            uint4 next[4];
-            auto fetch = [&](int c0) {
+            uint4 next[2];
+            auto fetch = [&](int col) {
 #pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    const int col = j.col0 + c0 + v * 8;
+                for (int v = 0; v < 2; ++v) {
                     next[v] = make_uint4(0u, 0u, 0u, 0u);
-                    if (valid && col < width) next[v] = load8(aux + col, aux_vec);
+                    if (valid && col + v * 8 < width) next[v] = load8(aux + col + v * 8, aux_vec);
                 }
             };
-            if (with_aux) fetch(hf * kHalf);
+            if (with_aux) fetch(cw);
             __syncwarp();
             if (!__all_sync(0xffffffffu, mbar_wait(&bars->accfull[buf], (tile >> 1) & 1, c.err,
                                                    abort_flag)))
@@ -437,97 +478,108 @@ __global__ void __launch_bounds__(kThreads, 1) exp_tc_kernel(const __grid_consta
             const bool has = j.steps1 > 0;   // otherwise the accumulators were not written
             float part = 0.f;
 #pragma unroll 1
-            for (int c0 = hf * kHalf; c0 < (hf + 1) * kHalf; c0 += 32) {
-                uint32_t r0[32], r1[32], r2[32];
-                uint4 now[4];
+            for (int c0 = pt * kPart; c0 < (pt + 1) * kPart; c0 += 16) {
+                const int col = j.col0 + c0;
+                if (col >= width) break;
+                const bool both = col + 8 < width;
+                uint32_t r0[16], r1[16], r2[16];
+                uint4 now[2];
                 __syncwarp();   // the loads below are warp-wide
-                tmem_ld32(acc + c0, r0);
-                if constexpr (GATED) tmem_ld32(acc + 128 + c0, r1);
-                if constexpr (C::kTwo) tmem_ld32(accq + c0, r2);
+                tmem_ld16(acc + c0, r0);
+                if constexpr (GATED) tmem_ld16(acc + 128 + c0, r1);
+                if constexpr (C::kTwo) tmem_ld16(accq + c0, r2);
                 if (with_aux) {
-#pragma unroll
-                    for (int v = 0; v < 4; ++v) now[v] = next[v];
-                    if (c0 + 32 < (hf + 1) * kHalf) fetch(c0 + 32);
+                    now[0] = next[0];
+                    now[1] = next[1];
+                    if (c0 + 16 < (pt + 1) * kPart) fetch(col + 16);
                 }
                 tmem_ld_wait();
-                const float *gb = gate_b + (c0 - hf * kHalf), *ub = up_b + (c0 - hf * kHalf);
+                const float *gb = gate_b + (c0 - pt * kPart), *ub = up_b + (c0 - pt * kPart);
+                float x[16];
 #pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    const int col = j.col0 + c0 + v * 8;
-                    if (col >= width) continue;
-                    float x[8], b8[8], u8[8], o8[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        x[i] = has ? __uint_as_float(r0[v * 8 + i]) : 0.f;
-                        if constexpr (C::kBias) b8[i] = gb[v * 8 + i];
-                        if constexpr (GATED) u8[i] = ub[v * 8 + i];
+                for (int i = 0; i < 16; ++i) x[i] = has ? __uint_as_float(r0[i]) : 0.f;
+                if constexpr (C::kGrad) {
+                    const int M = KIND == kDw2 ? s.o : s.first();
+                    T *out = (T *)(KIND == kDw2 ? c.dw2 : c.dw1);
+                    if (j.m0 + m < M)
+                        store16(out + ((size_t)j.expert * M + j.m0 + m) * width + col, x, both,
+                                wide);
+                } else if constexpr (KIND == kDx) {
+                    if (valid) {
+                        if (s.direct()) store16((T *)c.dx + tok * width + col, x, both, wide);
+                        else store16(c.slots + pair * width + col, x, both, true);
                     }
-                    if constexpr (KIND == kDaLin || KIND == kFirst || KIND == kSecond)
-                        if (with_aux) unpack8<T>(now[v], o8);
-                    if constexpr (C::kGrad) {
-                        const int M = KIND == kDw2 ? s.o : s.first();
-                        T *out = (T *)(KIND == kDw2 ? c.dw2 : c.dw1);
-                        if (j.m0 + m < M)
-                            store8(out + ((size_t)j.expert * M + j.m0 + m) * width + col, x);
-                    } else if constexpr (KIND == kDx) {
-                        if (valid) {
-                            if (s.direct()) store8((T *)c.dx + tok * width + col, x);
-                            else store8(c.slots + pair * width + col, x);
-                        }
-                    } else if constexpr (KIND == kDaLin || KIND == kDaMlp) {
-                        if (none || j.valid <= 0) continue;
-                        T *da = (T *)c.da + row * s.first() + col;
-                        float d1[8], d2[8], h8[8];
+                } else if constexpr (KIND == kDaLin || KIND == kDaMlp) {
+                    if (none || j.valid <= 0) continue;
+                    T *da = (T *)c.da + row * s.first() + col;
+                    const bool whole = width % 16 == 0;
+                    float o16[16], d2[16];
+                    if constexpr (KIND == kDaLin) {
+                        float lo[8], hi[8];
+                        unpack8<T>(now[0], lo);
+                        unpack8<T>(now[1], hi);
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
-                            float f, df, up = 1.f, qq;
-                            act_fast<ACT>(x[i] + b8[i], f, df);
-                            if constexpr (KIND == kDaMlp) qq = __uint_as_float(r2[v * 8 + i]);
-                            else qq = o8[i];
-                            if constexpr (GATED) up = __uint_as_float(r1[v * 8 + i]) + u8[i];
-                            const float gq = g * qq, fu = f * up;
-                            // rows past the segment are zeros: the weight
-                            // gradients contract over them
-                            part = fmaf(qq, fu, part);
-                            d1[i] = valid ? gq * up * df : 0.f;
-                            if constexpr (GATED) d2[i] = valid ? gq * f : 0.f;
-                            if constexpr (KIND == kDaMlp) h8[i] = valid ? g * fu : 0.f;
+                            o16[i] = lo[i];
+                            o16[8 + i] = hi[i];
                         }
-                        store8(da, d1);
-                        if constexpr (GATED) store8(da + width, d2);
-                        if constexpr (KIND == kDaMlp) store8((T *)c.hid + row * width + col, h8);
+                    }
+                    // (rows past the segment are written as zeros: the weight
+                    // gradients contract over them)
+                    const float gv = valid ? g : 0.f;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        float f, df, up = 1.f, qq;
+                        act_fast<ACT>(x[i] + gb[i], f, df);
+                        if constexpr (KIND == kDaMlp) qq = __uint_as_float(r2[i]);
+                        else qq = o16[i];
+                        if constexpr (GATED) up = __uint_as_float(r1[i]) + ub[i];
+                        const float gq = gv * qq, fu = f * up;
+                        if (both || i < 8) part = fmaf(qq, fu, part);
+                        x[i] = valid ? gq * up * df : 0.f;
+                        if constexpr (GATED) d2[i] = valid ? gq * f : 0.f;
+                        if constexpr (KIND == kDaMlp) o16[i] = valid ? gv * fu : 0.f;
+                    }
+                    store16(da, x, both, whole);
+                    if constexpr (GATED) store16(da + width, d2, both, whole);
+                    if constexpr (KIND == kDaMlp)
+                        store16((T *)c.hid + row * width + col, o16, both, whole);
+                } else {
+                    if (!valid) continue;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        x[i] += gb[i];
+                        if constexpr (KIND == kFirst) {
+                            float f, df;
+                            act_fast<ACT>(x[i], f, df);
+                            x[i] = f;
+                            if constexpr (GATED) x[i] *= __uint_as_float(r1[i]) + ub[i];
+                        }
+                    }
+                    if (KIND == kFirst && s.mlp) {
+                        // rounded to the type: the second product's operand
+                        if (!none)
+                            store16((T *)c.hid + row * width + col, x, both, width % 16 == 0);
+                    } else if (s.direct()) {
+                        float lo[8] = {}, hi[8] = {};
+                        if (with_res) {
+                            unpack8<T>(now[0], lo);
+                            unpack8<T>(now[1], hi);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float r = i < 8 ? lo[i & 7] : hi[i & 7];
+                            x[i] = none ? r : fmaf(g, x[i], r);
+                        }
+                        store16((T *)c.y + tok * width + col, x, both, wide);
                     } else {
-                        if (!valid) continue;
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            x[i] += b8[i];
-                            if constexpr (KIND == kFirst) {
-                                float f, df;
-                                act_fast<ACT>(x[i], f, df);
-                                x[i] = f;
-                                if constexpr (GATED)
-                                    x[i] *= __uint_as_float(r1[v * 8 + i]) + u8[i];
-                            }
-                        }
-                        if (KIND == kFirst && s.mlp) {
-                            // rounded to the type: the second product's operand
-                            if (!none) store8((T *)c.hid + row * width + col, x);
-                        } else if (s.direct()) {
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const float r = with_res ? o8[i] : 0.f;
-                                x[i] = none ? r : fmaf(g, x[i], r);
-                            }
-                            store8((T *)c.y + tok * width + col, x);
-                        } else {
-                            store8(c.slots + pair * width + col, x);
-                        }
+                        store16(c.slots + pair * width + col, x, both, true);
                     }
                 }
             }
             if constexpr (KIND == kDaLin || KIND == kDaMlp) {
-                if (valid && !none && c.dresp)
-                    c.rpart[row * c.nrpart + (j.col0 / C::NB) * 2 + hf] = part;
+                if (valid && !none && c.dresp && cw < width)
+                    c.rpart[row * c.nrpart + cw / kPart] = part;
             }
             tc_fence_before();
             __syncwarp();
@@ -548,9 +600,9 @@ __global__ void __launch_bounds__(kThreads, 1) exp_tc_kernel(const __grid_consta
 }
 
 // ------------------------------------------------------------- host side
-template <typename T, int KIND, int ACT, bool GATED, int CG>
+template <typename T, int KIND, int ACT, bool GATED, int CG, int W>
 cudaError_t launch_kind(const ExpCall &c, cudaStream_t st) {
-    using C = Cfg<KIND, GATED, CG>;
+    using C = Cfg<KIND, GATED, CG, W>;
     const ExpShape &s = c.s;
     Args a;
     a.c = c;
@@ -560,24 +612,24 @@ cudaError_t launch_kind(const ExpCall &c, cudaStream_t st) {
         case kFirst:
         case kDaLin:
             width = s.mlp ? s.h : s.o;
-            maps.make(&a.a, c.xrows, s.d, c.point_rows, 0, kRowsA);
+            maps.make(&a.a, c.xrows, s.d, c.point_rows, 0, C::kBoxA);
             maps.make(&a.b, c.w1, s.d, s.first(), s.K, GATED ? 128 : C::N1 / CG);
             break;
         case kDaMlp:
             width = s.h;
-            maps.make(&a.a, c.dyrows, s.o, c.point_rows, 0, kRowsA);
+            maps.make(&a.a, c.dyrows, s.o, c.point_rows, 0, C::kBoxA);
             maps.make(&a.b, c.w2, s.h, s.o, s.K, kStepK);
-            maps.make(&a.a2, c.xrows, s.d, c.point_rows, 0, kRowsA);
+            maps.make(&a.a2, c.xrows, s.d, c.point_rows, 0, C::kBoxA);
             maps.make(&a.b2, c.w1, s.d, s.first(), s.K, GATED ? 128 : C::N2 / CG);
             break;
         case kSecond:
             width = s.o;
-            maps.make(&a.a, c.hid, s.h, c.max_rows, 0, kRowsA);
+            maps.make(&a.a, c.hid, s.h, c.max_rows, 0, C::kBoxA);
             maps.make(&a.b, c.w2, s.h, s.o, s.K, C::N1 / CG);
             break;
         case kDx:
             width = s.d;
-            maps.make(&a.a, c.da, s.first(), c.max_rows, 0, kRowsA);
+            maps.make(&a.a, c.da, s.first(), c.max_rows, 0, C::kBoxA);
             maps.make(&a.b, c.w1, s.d, s.first(), s.K, kStepK);
             break;
         case kDw1:
@@ -599,7 +651,7 @@ cudaError_t launch_kind(const ExpCall &c, cudaStream_t st) {
     a.vec_res = ((uintptr_t)c.res & 15) == 0;
     const int64_t most = C::kGrad ? (int64_t)s.K * a.ntm * a.ntn : (int64_t)c.rt.max_tiles * a.ntn;
     if (most > 0x7fff0000) return cudaErrorNotSupported;
-    const auto kernel = exp_tc_kernel<T, KIND, ACT, GATED, CG>;
+    const auto kernel = exp_tc_kernel<T, KIND, ACT, GATED, CG, W>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)C::kSmem);
     if (e != cudaSuccess) return e;
@@ -638,15 +690,28 @@ cudaError_t launch_kind(const ExpCall &c, cudaStream_t st) {
 
 // Products whose rows are points run in pairs when the segments are long
 // enough (kExpPairRows); a weight gradient when its own rows fill pairs too.
+template <typename T, int KIND, int ACT, bool GATED, int W>
+cudaError_t launch_rows_w(const ExpCall &c, cudaStream_t st) {
+    return c.rt.tile_rows == 2 * kRowsA ? launch_kind<T, KIND, ACT, GATED, 2, W>(c, st)
+                                        : launch_kind<T, KIND, ACT, GATED, 1, W>(c, st);
+}
 template <typename T, int KIND, int ACT, bool GATED>
 cudaError_t launch_rows(const ExpCall &c, cudaStream_t st) {
-    return c.rt.tile_rows == 2 * kRowsA ? launch_kind<T, KIND, ACT, GATED, 2>(c, st)
-                                        : launch_kind<T, KIND, ACT, GATED, 1>(c, st);
+    const int width = KIND == kDx ? c.s.d : KIND == kSecond || !c.s.mlp ? c.s.o : 256;
+    if constexpr (KIND != kDaMlp && !GATED)
+        if (width <= 128) return launch_rows_w<T, KIND, ACT, GATED, 128>(c, st);
+    return launch_rows_w<T, KIND, ACT, GATED, 256>(c, st);
+}
+template <typename T, int KIND, int W>
+cudaError_t launch_grad_w(const ExpCall &c, cudaStream_t st) {
+    const int tiles = ((KIND == kDw2 ? c.s.o : c.s.first()) + kRowsA - 1) / kRowsA;
+    return c.rt.tile_rows == 2 * kRowsA && (tiles % 2 == 0 || tiles > 8)
+               ? launch_kind<T, KIND, GMM_ACT_NONE, false, 2, W>(c, st)
+               : launch_kind<T, KIND, GMM_ACT_NONE, false, 1, W>(c, st);
 }
 template <typename T, int KIND> cudaError_t launch_grad(const ExpCall &c, cudaStream_t st) {
-    const int tiles = ((KIND == kDw2 ? c.s.o : c.s.first()) + kRowsA - 1) / kRowsA;
-    return c.rt.tile_rows == 2 * kRowsA && (tiles % 2 == 0 || tiles > 8) ? launch_kind<T, KIND, GMM_ACT_NONE, false, 2>(c, st)
-                                       : launch_kind<T, KIND, GMM_ACT_NONE, false, 1>(c, st);
+    return (KIND == kDw2 ? c.s.h : c.s.d) <= 128 ? launch_grad_w<T, KIND, 128>(c, st)
+                                                 : launch_grad_w<T, KIND, 256>(c, st);
 }
 
 template <typename T, int ACT, bool GATED>
@@ -687,10 +752,10 @@ cudaError_t launch_exp_tc(const ExpCall &c, bool backward, cudaStream_t s) {
                               : act_tc<__half>(c, backward, s);
 }
 
-// Partial sums of dresp per row: two halves of each column tile.
+// Partial sums of dresp per row: one from each epilogue warp of a tile.
 int exp_tc_resp_parts(const ExpShape &s) {
-    const int nb = s.mlp ? 128 : 256;
-    return 2 * (((s.mlp ? s.h : s.o) + nb - 1) / nb);
+    const int width = s.mlp ? s.h : s.o, part = s.mlp || width <= 128 ? 32 : 64;
+    return (width + part - 1) / part;
 }
 
 }  // namespace gmmb
