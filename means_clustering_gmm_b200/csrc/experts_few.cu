@@ -334,8 +334,7 @@ __global__ void __launch_bounds__(kThreads, 4) few_first_kernel(ExpCall c) {
                 v += part[k][row][col];
                 if (GATED) u += part[k][16 + row][col];
             }
-            float f, df;
-            act_fast<ACT>(v + (b ? value_at(b + out) : 0.f), f, df);
+            float f = act_fast<ACT>(v + (b ? value_at(b + out) : 0.f));
             if (GATED) f *= u + (b ? value_at(b + width + out) : 0.f);
             const int64_t p = list[col0 + col];
             if (s.mlp) {

@@ -99,7 +99,6 @@ struct Args {
     ExpCall c;
     CUtensorMap a, b, a2, b2;   // phase 1 and phase 2 operands
     int ntn, ntm;               // column tiles; row tiles of one expert's dW
-    int vec_res;                // the residual may be read 16 bytes at a time
 };
 
 struct Bars {
@@ -149,18 +148,45 @@ __device__ __forceinline__ Job job_of(const Args &a, int idx, int rank) {
     return j;
 }
 
-// Eight consecutive elements, raw, and as floats.
-template <typename T> __device__ __forceinline__ uint4 load8(const T *p, bool vec) {
-    if (vec) return *reinterpret_cast<const uint4 *>(p);
-    __align__(16) T e[8];
+// Sixteen consecutive elements of a row, raw (the first eight where `both` is
+// false), and as floats.  wide: 32-byte aligned, one whole sector at once;
+// vec: 16-byte aligned.
+template <typename T>
+__device__ __forceinline__ void load16(const T *p, bool both, bool wide, bool vec,
+                                       uint32_t (&w)[8]) {
+    if (wide) {
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]),
+                       "=r"(w[6]), "=r"(w[7])
+                     : "l"(p));
+        return;
+    }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) e[i] = p[i];
-    return *reinterpret_cast<const uint4 *>(e);
+    for (int h = 0; h < 2; ++h) {
+        if (h == 1 && !both) break;
+        uint4 v;
+        if (vec) {
+            v = *reinterpret_cast<const uint4 *>(p + 8 * h);
+        } else {
+            __align__(16) T e[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) e[i] = p[8 * h + i];
+            v = *reinterpret_cast<const uint4 *>(e);
+        }
+        w[4 * h] = v.x;
+        w[4 * h + 1] = v.y;
+        w[4 * h + 2] = v.z;
+        w[4 * h + 3] = v.w;
+    }
 }
-template <typename T> __device__ __forceinline__ void unpack8(const uint4 &w, float (&v)[8]) {
-    const T *e = reinterpret_cast<const T *>(&w);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = to_float(e[i]);
+__device__ __forceinline__ float2 unpack2(uint32_t w, __half) {
+    return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+}
+__device__ __forceinline__ float2 unpack2(uint32_t w, __nv_bfloat16) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ float2 pair_of(const uint32_t (&r)[16], int i) {
+    return make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
 }
 template <typename T> __device__ __forceinline__ uint32_t pack2(float x, float y);
 template <> __device__ __forceinline__ uint32_t pack2<__half>(float x, float y) {
@@ -179,10 +205,10 @@ __device__ __forceinline__ void store32(void *p, const uint32_t (&w)[8]) {
 // Sixteen consecutive results (the first eight where `both` is false).
 // wide: 32-byte aligned, one whole sector in one store.
 template <typename T>
-__device__ __forceinline__ void store16(T *p, const float (&v)[16], bool both, bool wide) {
+__device__ __forceinline__ void store16(T *p, const float2 (&v)[8], bool both, bool wide) {
     uint32_t w[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = pack2<T>(v[2 * i], v[2 * i + 1]);
+    for (int i = 0; i < 8; ++i) w[i] = pack2<T>(v[i].x, v[i].y);
     if (wide) {
         store32(p, w);
         return;
@@ -191,15 +217,17 @@ __device__ __forceinline__ void store16(T *p, const float (&v)[16], bool both, b
     o[0] = make_uint4(w[0], w[1], w[2], w[3]);
     if (both) o[1] = make_uint4(w[4], w[5], w[6], w[7]);
 }
-__device__ __forceinline__ void store16(float *p, const float (&v)[16], bool both, bool) {
-    uint32_t w[8];
+__device__ __forceinline__ void store16(float *p, const float2 (&v)[8], bool both, bool) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(v[i]);
-    store32(p, w);
-    if (both) {
+    for (int h = 0; h < 2; ++h) {
+        if (h == 1 && !both) break;
+        uint32_t w[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(v[8 + i]);
-        store32(p + 8, w);
+        for (int i = 0; i < 4; ++i) {
+            w[2 * i] = __float_as_uint(v[4 * h + i].x);
+            w[2 * i + 1] = __float_as_uint(v[4 * h + i].y);
+        }
+        store32(p + 8 * h, w);
     }
 }
 
@@ -428,7 +456,9 @@ __global__ void __launch_bounds__(kThreads, 1) exp_tc_kernel(const __grid_consta
         // this kind reads a row of another array beside the accumulators
         const bool with_res = (KIND == kSecond || (KIND == kFirst && !s.mlp)) && s.direct() && c.res;
         const bool with_aux = KIND == kDaLin || with_res;
-        const bool aux_vec = KIND == kDaLin || a.vec_res;
+        const void *aux0 = KIND == kDaLin ? c.dy : c.res;
+        const bool aux_vec = ((uintptr_t)aux0 & 15) == 0;
+        const bool aux_wide = width % 16 == 0 && ((uintptr_t)aux0 & 31) == 0;
         // (workspace rows are aligned; the caller's arrays may be to 16 bytes)
         const void *dst = KIND == kDw1 ? c.dw1 : KIND == kDw2 ? c.dw2 : KIND == kDx ? c.dx : c.y;
         const bool wide = width % 16 == 0 && ((uintptr_t)dst & 31) == 0;
@@ -457,14 +487,11 @@ __global__ void __launch_bounds__(kThreads, 1) exp_tc_kernel(const __grid_consta
                 }
             }
             // the other array's row, 16 columns ahead of their use
-            const T *aux = (const T *)(KIND == kDaLin ? c.dy : c.res) + tok * width;
-            uint4 next[2];
+            const T *aux = (const T *)aux0 + tok * width;
+            uint32_t next[8] = {};
             auto fetch = [&](int col) {
-#pragma unroll
-                for (int v = 0; v < 2; ++v) {
-                    next[v] = make_uint4(0u, 0u, 0u, 0u);
-                    if (valid && col + v * 8 < width) next[v] = load8(aux + col + v * 8, aux_vec);
-                }
+                if (valid && col < width)
+                    load16(aux + col, col + 8 < width, aux_wide, aux_vec, next);
             };
             if (with_aux) fetch(cw);
             __syncwarp();
@@ -483,21 +510,42 @@ __global__ void __launch_bounds__(kThreads, 1) exp_tc_kernel(const __grid_consta
                 if (col >= width) break;
                 const bool both = col + 8 < width;
                 uint32_t r0[16], r1[16], r2[16];
-                uint4 now[2];
+                uint32_t now[8];
                 __syncwarp();   // the loads below are warp-wide
                 tmem_ld16(acc + c0, r0);
                 if constexpr (GATED) tmem_ld16(acc + 128 + c0, r1);
                 if constexpr (C::kTwo) tmem_ld16(accq + c0, r2);
                 if (with_aux) {
-                    now[0] = next[0];
-                    now[1] = next[1];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) now[i] = next[i];
                     if (c0 + 16 < (pt + 1) * kPart) fetch(col + 16);
                 }
                 tmem_ld_wait();
-                const float *gb = gate_b + (c0 - pt * kPart), *ub = up_b + (c0 - pt * kPart);
-                float x[16];
+                float2 x[8];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) x[i] = has ? __uint_as_float(r0[i]) : 0.f;
+                for (int i = 0; i < 8; ++i) x[i] = pair_of(r0, i);
+                if (!has)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[i] = splat(0.f);
+                if constexpr (C::kBias) {
+                    const float4 *gb = reinterpret_cast<const float4 *>(gate_b + c0 - pt * kPart);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float4 b = gb[i];
+                        x[2 * i] = __fadd2_rn(x[2 * i], make_float2(b.x, b.y));
+                        x[2 * i + 1] = __fadd2_rn(x[2 * i + 1], make_float2(b.z, b.w));
+                    }
+                }
+                float2 up[8];
+                if constexpr (GATED) {
+                    const float4 *ub = reinterpret_cast<const float4 *>(up_b + c0 - pt * kPart);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float4 b = ub[i];
+                        up[2 * i] = __fadd2_rn(pair_of(r1, 2 * i), make_float2(b.x, b.y));
+                        up[2 * i + 1] = __fadd2_rn(pair_of(r1, 2 * i + 1), make_float2(b.z, b.w));
+                    }
+                }
                 if constexpr (C::kGrad) {
                     const int M = KIND == kDw2 ? s.o : s.first();
                     T *out = (T *)(KIND == kDw2 ? c.dw2 : c.dw1);
@@ -513,47 +561,43 @@ __global__ void __launch_bounds__(kThreads, 1) exp_tc_kernel(const __grid_consta
                     if (none || j.valid <= 0) continue;
                     T *da = (T *)c.da + row * s.first() + col;
                     const bool whole = width % 16 == 0;
-                    float o16[16], d2[16];
-                    if constexpr (KIND == kDaLin) {
-                        float lo[8], hi[8];
-                        unpack8<T>(now[0], lo);
-                        unpack8<T>(now[1], hi);
+                    float2 hs[8], d2[8], sum = splat(0.f);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            o16[i] = lo[i];
-                            o16[8 + i] = hi[i];
+                    for (int i = 0; i < 8; ++i) {
+                        float2 f, df, qq;
+                        act_pair<ACT>(x[i], f, df);
+                        if constexpr (KIND == kDaMlp) qq = pair_of(r2, i);
+                        else qq = unpack2(now[i], T{});
+                        const float2 gq = __fmul2_rn(splat(g), qq);
+                        float2 fu = f, du = df;
+                        if constexpr (GATED) {
+                            fu = __fmul2_rn(f, up[i]);
+                            du = __fmul2_rn(df, up[i]);
+                            d2[i] = __fmul2_rn(gq, f);
                         }
+                        if (i < 4 || both) sum = __ffma2_rn(qq, fu, sum);
+                        x[i] = __fmul2_rn(gq, du);
+                        if constexpr (KIND == kDaMlp) hs[i] = __fmul2_rn(splat(g), fu);
                     }
-                    // (rows past the segment are written as zeros: the weight
-                    // gradients contract over them)
-                    const float gv = valid ? g : 0.f;
+                    part += sum.x + sum.y;
+                    // rows past the segment are zeros: the weight gradients
+                    // contract over them
+                    if (!valid)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        float f, df, up = 1.f, qq;
-                        act_fast<ACT>(x[i] + gb[i], f, df);
-                        if constexpr (KIND == kDaMlp) qq = __uint_as_float(r2[i]);
-                        else qq = o16[i];
-                        if constexpr (GATED) up = __uint_as_float(r1[i]) + ub[i];
-                        const float gq = gv * qq, fu = f * up;
-                        if (both || i < 8) part = fmaf(qq, fu, part);
-                        x[i] = valid ? gq * up * df : 0.f;
-                        if constexpr (GATED) d2[i] = valid ? gq * f : 0.f;
-                        if constexpr (KIND == kDaMlp) o16[i] = valid ? gv * fu : 0.f;
-                    }
+                        for (int i = 0; i < 8; ++i) x[i] = d2[i] = hs[i] = splat(0.f);
                     store16(da, x, both, whole);
                     if constexpr (GATED) store16(da + width, d2, both, whole);
                     if constexpr (KIND == kDaMlp)
-                        store16((T *)c.hid + row * width + col, o16, both, whole);
+                        store16((T *)c.hid + row * width + col, hs, both, whole);
                 } else {
                     if (!valid) continue;
+                    if constexpr (KIND == kFirst) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        x[i] += gb[i];
-                        if constexpr (KIND == kFirst) {
-                            float f, df;
-                            act_fast<ACT>(x[i], f, df);
+                        for (int i = 0; i < 8; ++i) {
+                            float2 f, df;
+                            act_pair<ACT>(x[i], f, df);
                             x[i] = f;
-                            if constexpr (GATED) x[i] *= __uint_as_float(r1[i]) + ub[i];
+                            if constexpr (GATED) x[i] = __fmul2_rn(f, up[i]);
                         }
                     }
                     if (KIND == kFirst && s.mlp) {
@@ -561,15 +605,13 @@ __global__ void __launch_bounds__(kThreads, 1) exp_tc_kernel(const __grid_consta
                         if (!none)
                             store16((T *)c.hid + row * width + col, x, both, width % 16 == 0);
                     } else if (s.direct()) {
-                        float lo[8] = {}, hi[8] = {};
-                        if (with_res) {
-                            unpack8<T>(now[0], lo);
-                            unpack8<T>(now[1], hi);
-                        }
+                        // (a point without an expert: what the sum over none gives)
+                        const float gv = none ? 0.f : g;
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float r = i < 8 ? lo[i & 7] : hi[i & 7];
-                            x[i] = none ? r : fmaf(g, x[i], r);
+                        for (int i = 0; i < 8; ++i) {
+                            if (none) x[i] = splat(0.f);
+                            x[i] = __ffma2_rn(splat(gv), x[i],
+                                              with_res ? unpack2(now[i], T{}) : splat(0.f));
                         }
                         store16((T *)c.y + tok * width + col, x, both, wide);
                     } else {
@@ -648,7 +690,6 @@ cudaError_t launch_kind(const ExpCall &c, cudaStream_t st) {
     if (!maps.ok) return cudaErrorNotSupported;
     a.ntn = (width + C::NB - 1) / C::NB;
     a.ntm = (mrows + C::kTileRows - 1) / C::kTileRows;
-    a.vec_res = ((uintptr_t)c.res & 15) == 0;
     const int64_t most = C::kGrad ? (int64_t)s.K * a.ntm * a.ntn : (int64_t)c.rt.max_tiles * a.ntn;
     if (most > 0x7fff0000) return cudaErrorNotSupported;
     const auto kernel = exp_tc_kernel<T, KIND, ACT, GATED, CG, W>;
