@@ -50,7 +50,7 @@ int path_of(const ExpShape &p, bool backward, uint32_t flags) {
 }
 
 struct Layout {
-    size_t cnt, seg, tile_expert, pair_at, ntiles, row_pair, hist, hid, da, xrows, dyrows, slots, rpart, colpart, total;
+    size_t cnt, seg, tile_at, pair_at, ntiles, row_pair, hist, hid, da, xrows, dyrows, slots, rpart, colpart, total;
     int64_t max_rows;
     int max_tiles, nrpart;
     size_t esize;
@@ -74,8 +74,8 @@ Layout layout_of(const ExpShape &p, bool backward, int path) {
     const size_t chunks = p.dense ? 0 : (size_t)((p.P + 255) / 256);
     take(L.cnt, p.dense ? 0 : KK * 4);
     take(L.seg, p.dense ? 0 : (KK + 1) * 4);
-    take(L.tile_expert, p.dense ? 0 : (size_t)L.max_tiles * 4);
-    take(L.pair_at, p.dense ? 0 : (size_t)L.max_tiles * 8);
+    take(L.tile_at, p.dense ? 0 : (size_t)L.max_tiles * 16);
+    take(L.pair_at, p.dense ? 0 : (size_t)L.max_tiles * 16);
     take(L.ntiles, 8);
     take(L.row_pair, p.dense ? 0 : (size_t)L.max_rows * 4);
     take(L.hist, chunks * KK * 4);
@@ -105,8 +105,8 @@ ExpCall make_call(const ExpShape &p, const Layout &L, void *ws, const int32_t *i
     c.err = (int *)b;
     c.rt.cnt = (int *)(b + L.cnt);
     c.rt.seg = (int *)(b + L.seg);
-    c.rt.tile_expert = (int *)(b + L.tile_expert);
-    c.rt.pair_at = (int2 *)(b + L.pair_at);
+    c.rt.tile_at = (int4 *)(b + L.tile_at);
+    c.rt.pair_at = (int4 *)(b + L.pair_at);
     c.rt.ntiles = (int *)(b + L.ntiles);
     c.rt.row_pair = (int *)(b + L.row_pair);
     c.rt.hist = (int *)(b + L.hist);

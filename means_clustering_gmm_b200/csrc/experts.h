@@ -34,8 +34,8 @@ constexpr int64_t kExpPairRows = 384;
 struct ExpRoute {
     int *cnt;           // [K + 1] pairs of each expert; [K]: points without any (direct only)
     int *seg;           // [K + 2] first row of each segment
-    int *tile_expert;   // [max_tiles] expert of each 128-row tile
-    int2 *pair_at;      // [max_tiles] expert and first row of each 256-row tile
+    int4 *tile_at;      // [max_tiles] expert, first row, valid rows of each 128-row tile
+    int4 *pair_at;      // [max_tiles] the same of each 256-row tile
     int *ntiles;        // [2] 128-row and 256-row tiles
     int *row_pair;      // [max rows] pair of each valid row
     int *hist;          // [chunks x (K + 1)]
@@ -45,28 +45,19 @@ struct ExpRoute {
     int max_tiles;      // of 128 rows
     int tile_rows;      // of the products' tiles
 
-    struct Tile { int expert, valid; int64_t row0, seg_end; };
+    struct Tile { int expert, valid; int64_t row0; };
     __device__ __forceinline__ int tiles(int rows = kExpTile) const {
         return ids ? ntiles[rows == kExpTile ? 0 : 1] : (int)((N + rows - 1) / rows);
     }
+    // a tile's entry, loaded, and what it says
+    __device__ __forceinline__ int4 tile_entry(int t, int rows = kExpTile) const {
+        if (ids) return rows == kExpTile ? tile_at[t] : pair_at[t];
+        const int64_t left = N - (int64_t)t * rows;
+        return make_int4(0, t * rows, left < rows ? (int)left : rows, 0);
+    }
     __device__ __forceinline__ Tile tile(int t, int rows = kExpTile) const {
-        Tile x;
-        x.expert = 0;
-        x.row0 = (int64_t)t * rows;
-        x.seg_end = N;
-        if (ids) {
-            if (rows == kExpTile) {
-                x.expert = tile_expert[t];
-            } else {
-                const int2 at = pair_at[t];
-                x.expert = at.x;
-                x.row0 = at.y;
-            }
-            x.seg_end = (int64_t)seg[x.expert] + cnt[x.expert];
-        }
-        const int64_t v = x.seg_end - x.row0;
-        x.valid = v < rows ? (int)v : rows;
-        return x;
+        const int4 e = tile_entry(t, rows);
+        return Tile{e.x, e.z, e.y};
     }
     __device__ __forceinline__ int64_t pair(int64_t row) const {
         return ids ? row_pair[row] : row;

@@ -136,8 +136,10 @@ __device__ __forceinline__ void make_tiles(const ExpRoute &rt, const int *cnt, i
             const int mid = (lo + hi) >> 1;
             if (f[mid] <= t) lo = mid; else hi = mid;
         }
-        if (two) rt.pair_at[t] = make_int2(lo, (first1[lo] + 2 * (t - f[lo])) * kExpTile);
-        else rt.tile_expert[t] = lo;
+        const int rows = two ? 2 * kExpTile : kExpTile, before = (t - f[lo]) * rows;
+        const int left = cnt[lo] - before;
+        (two ? rt.pair_at : rt.tile_at)[t] =
+            make_int4(lo, first1[lo] * kExpTile + before, left < rows ? left : rows, 0);
     }
 }
 
@@ -299,7 +301,7 @@ exp_gather_kernel(ExpRoute rt, const uint4 *__restrict__ x, uint4 *__restrict__ 
         const auto t = rt.tile((int)(row / kExpTile));
         if (t.expert >= rt.K) continue;
         uint4 *o = dst + row * u;
-        if (row < t.seg_end) {
+        if (row < t.row0 + t.valid) {
             const uint4 *p = src + rt.token(rt.pair(row)) * u;
             int i = lane;
             for (; i + 96 < u; i += 128) {
@@ -426,7 +428,7 @@ exp_dresp_kernel(ExpRoute rt, const float *__restrict__ part, int nparts, const 
     const int64_t rows = (int64_t)rt.tiles() * kExpTile;
     for (int64_t row = blockIdx.x * 8 + (threadIdx.x >> 5); row < rows; row += gridDim.x * 8) {
         const auto t = rt.tile((int)(row / kExpTile));
-        if (row >= t.seg_end || t.expert >= rt.K) continue;
+        if (row >= t.row0 + t.valid || t.expert >= rt.K) continue;
         const int64_t p = rt.pair(row);
         float acc = 0.f;
         for (int i = lane; i < nparts; i += 32) acc += part[row * nparts + i];

@@ -119,29 +119,40 @@ __device__ __forceinline__ int total_jobs(const Args &a) {
                                        : a.c.rt.tiles(CG * kRowsA) * a.ntn;
 }
 
+// What a job needs from memory: loaded a job ahead, one independent load (a
+// chain of them at every tile left the products waiting).
 template <int KIND, bool GATED, int CG, int W>
-__device__ __forceinline__ Job job_of(const Args &a, int idx, int rank) {
+__device__ __forceinline__ int4 job_entry(const Args &a, int idx, int total) {
+    if (idx >= total) return make_int4(0, 0, 0, 0);
+    const int t = idx / a.ntn;
+    if constexpr (Cfg<KIND, GATED, CG, W>::kGrad) {
+        const int e = t / a.ntm;
+        return a.c.rt.ids ? make_int4(e, a.c.rt.seg[e], a.c.rt.cnt[e], 0)
+                          : make_int4(0, 0, (int)a.c.rt.N, 0);
+    } else {
+        return a.c.rt.tile_entry(t, CG * kRowsA);
+    }
+}
+template <int KIND, bool GATED, int CG, int W>
+__device__ __forceinline__ Job job_of(const Args &a, int idx, int rank, const int4 &e) {
     using C = Cfg<KIND, GATED, CG, W>;
     Job j;
     const ExpShape &s = a.c.s;
     const int t = idx / a.ntn;
     j.col0 = (idx - t * a.ntn) * C::NB;
+    j.expert = e.x;
     if constexpr (C::kGrad) {
-        j.expert = t / a.ntm;
-        j.m0 = (t - j.expert * a.ntm) * C::kTileRows + rank * kRowsA;
-        const int64_t cnt = a.c.rt.ids ? a.c.rt.cnt[j.expert] : a.c.rt.N;
-        j.row0 = a.c.rt.ids ? a.c.rt.seg[j.expert] : 0;
+        j.m0 = t % a.ntm * C::kTileRows + rank * kRowsA;
+        j.row0 = e.y;
         j.valid = kRowsA;
-        j.steps1 = (int)((cnt + kStepK - 1) / kStepK);
+        j.steps1 = (e.z + kStepK - 1) / kStepK;
         j.steps2 = 0;
     } else {
-        const auto x = a.c.rt.tile(t, CG * kRowsA);
-        j.expert = x.expert;
-        j.row0 = x.row0 + rank * kRowsA;
-        j.valid = x.valid - rank * kRowsA < kRowsA ? x.valid - rank * kRowsA : kRowsA;
+        j.row0 = (int64_t)e.y + rank * kRowsA;
+        j.valid = e.z - rank * kRowsA < kRowsA ? e.z - rank * kRowsA : kRowsA;
         j.m0 = 0;
         const int k1 = KIND == kSecond ? s.h : KIND == kDx ? s.first() : C::kTwo ? s.o : s.d;
-        const bool none = x.expert >= s.K;
+        const bool none = j.expert >= s.K;
         j.steps1 = none ? 0 : (k1 + kStepK - 1) / kStepK;
         j.steps2 = C::kTwo && !none ? (s.d + kStepK - 1) / kStepK : 0;
     }
@@ -285,79 +296,82 @@ __global__ void __launch_bounds__(kThreads, 1) exp_tc_kernel(const __grid_consta
         // bytes are all counted on the barrier of rank 0, whose one arrival
         // expects both CTAs' (a slot is refilled only after the products that
         // read it, so no copy of a later phase can reach an earlier one).
-        uint32_t fill = 0;   // stages filled so far
+        // The loop is one thread's chain of instructions and was the bound
+        // when it recomputed its addresses (660 clocks a stage whose products
+        // take 256).
         if (lane == 0) {
+            const uint32_t sm0 = smem_u32(sm);
+            const uint32_t full0 = CG == 2 ? mapa_u32(&bars->full[0], 0)
+                                           : smem_u32(&bars->full[0]);
+            uint32_t slot = 0, parity = 1, fill = 0;
             bool ok = true;
+            // the next slot, free and expecting `bytes` from this CTA
+            auto open = [&](uint32_t bytes) {
+                ok = mbar_wait(&bars->empty[slot], parity, c.err, abort_flag);
+                if (ok && rank == 0) mbar_arrive_expect_tx(&bars->full[slot], CG * bytes);
+                return ok;
+            };
+            auto next = [&] {
+                ++fill;
+                if (++slot == (uint32_t)C::kStages) {
+                    slot = 0;
+                    parity ^= 1;
+                }
+            };
+            int4 entry = job_entry<KIND, GATED, CG, W>(a, first, total);
             for (int idx = first; idx < total && ok; idx += stride) {
-                const Job j = job_of<KIND, GATED, CG, W>(a, idx, rank);
-                const int steps = j.steps1 + j.steps2, row = (int)j.row0;
-                for (int st = 0; st < steps; ++st, ++fill) {
-                    const int slot = fill % C::kStages;
-                    ok = mbar_wait(&bars->empty[slot], ((fill / C::kStages) & 1) ^ 1, c.err,
-                                   abort_flag);
-                    if (!ok) break;
-                    uint8_t *A = sm + (size_t)slot * C::kStage, *B = A + kBytesA;
-                    const bool second = C::kTwo && st >= j.steps1;
-                    if (rank == 0)
-                        mbar_arrive_expect_tx(
-                            &bars->full[slot],
-                            CG * ((second ? C::kB2 : C::kB1) +
-                                  (C::kSmallA ? (j.valid + 31) / 32 * (kBytesA / 4) : kBytesA)));
-                    const uint32_t bar = CG == 2 ? mapa_u32(&bars->full[slot], 0)
-                                                 : smem_u32(&bars->full[slot]);
-                    auto box2 = [&](uint8_t *dst, const CUtensorMap *m, int x, int y) {
-                        if constexpr (CG == 2) tma_g2s_2d_pair(dst, m, x, y, bar);
-                        else tma_g2s_2d(dst, m, x, y, &bars->full[slot]);
-                    };
-                    auto box3 = [&](uint8_t *dst, const CUtensorMap *m, int x, int y) {
-                        if constexpr (CG == 2) tma_g2s_3d_pair(dst, m, x, y, j.expert, bar);
-                        else tma_g2s_3d(dst, m, x, y, j.expert, &bars->full[slot]);
-                    };
-                    const int k = (second ? st - j.steps1 : st) * kStepK;
-                    auto rows_a = [&](const CUtensorMap *m) {
-                        if constexpr (C::kSmallA) {
-                            for (int i = 0; i * 32 < j.valid; ++i)
-                                box2(A + i * (kBytesA / 4), m, k, row + i * 32);
-                        } else {
-                            box2(A, m, k, row);
-                        }
-                    };
-                    // this CTA's first column of B in a phase of N columns
-                    const int n1 = j.col0 + rank * (C::N1 / CG);
+                const Job j = job_of<KIND, GATED, CG, W>(a, idx, rank, entry);
+                entry = job_entry<KIND, GATED, CG, W>(a, idx + stride, total);
+                const int row = (int)j.row0;
+                const int groups = C::kSmallA ? (j.valid + 31) / 32 : 1;
+                const uint32_t bytes_a = C::kSmallA ? groups * (kBytesA / 4) : kBytesA;
+                // this CTA's first column of B in a phase of N columns
+                const int n1 = j.col0 + rank * (C::N1 / CG);
+                for (int st = 0, k = 0; st < j.steps1; ++st, k += kStepK) {
+                    if (!open(bytes_a + C::kB1)) break;
+                    const uint32_t A = sm0 + slot * C::kStage, B = A + kBytesA;
+                    const uint32_t bar = full0 + slot * 8;
                     if constexpr (C::kGrad) {
 #pragma unroll
                         for (int i = 0; i < kRowsA / 64; ++i)
-                            box2(A + i * kBlk, &a.a, j.m0 + i * 64, row + k);
+                            tma_g2s_2d<CG == 2>(A + i * kBlk, &a.a, j.m0 + i * 64, row + k, bar);
 #pragma unroll
                         for (int i = 0; i < C::N1 / CG / 64; ++i)
-                            box2(B + i * kBlk, &a.b, n1 + i * 64, row + k);
-                    } else if (!second) {
-                        rows_a(&a.a);
+                            tma_g2s_2d<CG == 2>(B + i * kBlk, &a.b, n1 + i * 64, row + k, bar);
+                    } else {
+                        for (int i = 0; i < groups; ++i)
+                            tma_g2s_2d<CG == 2>(A + i * (kBytesA / 4), &a.a, k, row + i * 32, bar);
                         if constexpr (C::kBMn1) {
 #pragma unroll
                             for (int i = 0; i < C::N1 / CG / 64; ++i)
-                                box3(B + i * kBlk, &a.b, n1 + i * 64, k);
+                                tma_g2s_3d<CG == 2>(B + i * kBlk, &a.b, n1 + i * 64, k, j.expert,
+                                                    bar);
                         } else if constexpr (KIND == kFirst && GATED) {
                             // the tile's gate rows, then its up rows: one each
                             // for a pair's CTAs
-                            if constexpr (CG == 2) {
-                                box3(B, &a.b, k, j.col0 + rank * s.h);
-                            } else {
-                                box3(B, &a.b, k, j.col0);
-                                box3(B + C::kB1 / 2, &a.b, k, j.col0 + s.h);
-                            }
+                            tma_g2s_3d<CG == 2>(B, &a.b, k, j.col0 + rank * s.h, j.expert, bar);
+                            if constexpr (CG == 1)
+                                tma_g2s_3d<false>(B + C::kB1 / 2, &a.b, k, j.col0 + s.h, j.expert,
+                                                  bar);
                         } else {
-                            box3(B, &a.b, k, n1);
+                            tma_g2s_3d<CG == 2>(B, &a.b, k, n1, j.expert, bar);
                         }
-                    } else {
-                        rows_a(&a.a2);
-                        if constexpr (GATED && CG == 1) {
-                            box3(B, &a.b2, k, j.col0);
-                            box3(B + C::kB2 / 2, &a.b2, k, j.col0 + s.h);
-                        } else {
-                            box3(B, &a.b2, k,
-                                 j.col0 + (GATED ? rank * s.h : rank * (C::N2 / CG)));
-                        }
+                    }
+                    next();
+                }
+                if constexpr (C::kTwo) {
+                    const int n2 = j.col0 + (GATED ? rank * s.h : rank * (C::N2 / CG));
+                    for (int st = 0, k = 0; st < j.steps2 && ok; ++st, k += kStepK) {
+                        if (!open(bytes_a + C::kB2)) break;
+                        const uint32_t A = sm0 + slot * C::kStage, B = A + kBytesA;
+                        const uint32_t bar = full0 + slot * 8;
+                        for (int i = 0; i < groups; ++i)
+                            tma_g2s_2d<CG == 2>(A + i * (kBytesA / 4), &a.a2, k, row + i * 32, bar);
+                        tma_g2s_3d<CG == 2>(B, &a.b2, k, n2, j.expert, bar);
+                        if constexpr (GATED && CG == 1)
+                            tma_g2s_3d<false>(B + C::kB2 / 2, &a.b2, k, j.col0 + s.h, j.expert,
+                                              bar);
+                        next();
                     }
                 }
             }
@@ -397,43 +411,43 @@ __global__ void __launch_bounds__(kThreads, 1) exp_tc_kernel(const __grid_consta
                 else
                     return mbar_wait(&bars->accfree[buf], parity, c.err, abort_flag);
             };
-            uint32_t use = 0, tile = 0;
+            uint32_t slot = 0, parity = 0, tile = 0;
             bool ok = true;
-            int idx = first;
-            Job nxt = idx < total ? job_of<KIND, GATED, CG, W>(a, idx, 0) : Job{};
-            for (; idx < total && ok; idx += stride, ++tile) {
-                const Job j = nxt;
-                if (idx + stride < total) nxt = job_of<KIND, GATED, CG, W>(a, idx + stride, 0);
+            // one stage's products into d; `fresh`: the first overwrites
+            auto stage = [&](uint32_t d, uint64_t dB, uint32_t id, uint32_t step_b, bool fresh) {
+                ok = mbar_wait(&bars->full[slot], parity, c.err, abort_flag);
+                if (!ok) return;
+                tc_fence_after();
+                const uint32_t off = slot * (C::kStage >> 4);
+#pragma unroll
+                for (uint32_t kk = 0; kk < kStepK / 16; ++kk)
+                    product(d, dA + off + kk * ((C::kAMn ? 2048 : 32) >> 4), dB + off + kk * step_b,
+                            id, !fresh || kk > 0);
+                commit(&bars->empty[slot]);
+                if (++slot == (uint32_t)C::kStages) {
+                    slot = 0;
+                    parity ^= 1;
+                }
+            };
+            int4 entry = job_entry<KIND, GATED, CG, W>(a, first, total);
+            for (int idx = first; idx < total && ok; idx += stride, ++tile) {
+                const Job j = job_of<KIND, GATED, CG, W>(a, idx, 0, entry);
+                entry = job_entry<KIND, GATED, CG, W>(a, idx + stride, total);
                 const int buf = tile & 1;
                 if (!free_wait(buf, ((tile >> 1) & 1) ^ 1)) break;
                 tc_fence_after();
-                const int steps = j.steps1 + j.steps2;
-                for (int st = 0; st < steps; ++st, ++use) {
-                    const bool second = C::kTwo && st >= j.steps1;
+                const uint32_t d1 = tmem + C::col1(tile);
+                for (int st = 0; st < j.steps1 && ok; ++st)
+                    stage(d1, dB1, id1, (C::kBMn1 ? 2048 : 32) >> 4, st == 0);
+                if constexpr (C::kTwo) {
                     // the single phase-2 accumulator: the tile before is read
-                    if (C::kTwo && GATED && st == j.steps1 && tile > 0) {
+                    if (GATED && ok && tile > 0 && j.steps2 > 0) {
                         ok = free_wait((tile - 1) & 1, ((tile - 1) >> 1) & 1);
-                        if (!ok) break;
                         tc_fence_after();
                     }
-                    const int slot = use % C::kStages;
-                    ok = mbar_wait(&bars->full[slot], (use / C::kStages) & 1, c.err, abort_flag);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t off = (uint32_t)(slot * C::kStage) >> 4;
-                    const bool fresh = st == 0 || (C::kTwo && st == j.steps1);
-#pragma unroll
-                    for (int kk = 0; kk < kStepK / 16; ++kk) {
-                        const uint64_t da = dA + off + (uint32_t)(kk * (C::kAMn ? 2048 : 32) >> 4);
-                        if (second)
-                            product(tmem + C::col2(tile), da, dB2 + off + (uint32_t)(kk * 32 >> 4),
-                                    id2, !fresh || kk > 0);
-                        else
-                            product(tmem + C::col1(tile), da,
-                                    dB1 + off + (uint32_t)(kk * (C::kBMn1 ? 2048 : 32) >> 4), id1,
-                                    !fresh || kk > 0);
-                    }
-                    commit(&bars->empty[slot]);
+                    const uint32_t d2 = tmem + C::col2(tile);
+                    for (int st = 0; st < j.steps2 && ok; ++st)
+                        stage(d2, dB2, id2, 32 >> 4, st == 0);
                 }
                 if (ok) commit(&bars->accfull[buf]);
             }
@@ -463,8 +477,10 @@ __global__ void __launch_bounds__(kThreads, 1) exp_tc_kernel(const __grid_consta
         const void *dst = KIND == kDw1 ? c.dw1 : KIND == kDw2 ? c.dw2 : KIND == kDx ? c.dx : c.y;
         const bool wide = width % 16 == 0 && ((uintptr_t)dst & 31) == 0;
         uint32_t tile = 0;
+        int4 entry = job_entry<KIND, GATED, CG, W>(a, first, total);
         for (int idx = first; idx < total; idx += stride, ++tile) {
-            const Job j = job_of<KIND, GATED, CG, W>(a, idx, rank);
+            const Job j = job_of<KIND, GATED, CG, W>(a, idx, rank, entry);
+            entry = job_entry<KIND, GATED, CG, W>(a, idx + stride, total);
             const int buf = tile & 1, cw = j.col0 + pt * kPart;   // this warp's first column
             const bool none = !C::kGrad && j.expert >= s.K;
             const bool valid = m < j.valid;

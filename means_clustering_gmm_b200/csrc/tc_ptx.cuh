@@ -118,41 +118,42 @@ __device__ __forceinline__ void bulk_prefetch_l2(const void *src_gmem, uint32_t 
 }
 
 // ------------------------------------------------- tensor-map copies
-// One box of a 2-D / 3-D tensor map -> shared, bytes counted on `bar`;
-// elements outside the tensor arrive as zeros.
-__device__ __forceinline__ void tma_g2s_2d(void *dst_smem, const void *map, int x, int y,
-                                           uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%2, %3}], [%4];"
-        ::"r"(smem_u32(dst_smem)), "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
-        : "memory");
+// One box of a 2-D / 3-D tensor map -> shared (addresses as shared-space
+// integers, which the issuing thread can step through cheaply), bytes counted
+// on `bar`; elements outside the tensor arrive as zeros.  PAIR: the bytes are
+// counted on a barrier of either CTA of the pair (its shared::cluster
+// address); the data goes to this CTA's shared memory.
+template <bool PAIR>
+__device__ __forceinline__ void tma_g2s_2d(uint32_t dst, const void *map, int x, int y,
+                                           uint32_t bar) {
+    if constexpr (PAIR)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::"
+            "bytes [%0], [%1, {%2, %3}], [%4];"
+            ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes "
+            "[%0], [%1, {%2, %3}], [%4];"
+            ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar)
+            : "memory");
 }
-__device__ __forceinline__ void tma_g2s_3d(void *dst_smem, const void *map, int x, int y, int z,
-                                           uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%2, %3, %4}], [%5];"
-        ::"r"(smem_u32(dst_smem)), "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
-        : "memory");
-}
-// The same into this CTA's shared memory with the bytes counted on a barrier
-// of either CTA of the pair (`cbar`: its shared::cluster address).
-__device__ __forceinline__ void tma_g2s_2d_pair(void *dst_smem, const void *map, int x, int y,
-                                                uint32_t cbar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%2, %3}], [%4];"
-        ::"r"(smem_u32(dst_smem)), "l"(map), "r"(x), "r"(y), "r"(cbar)
-        : "memory");
-}
-__device__ __forceinline__ void tma_g2s_3d_pair(void *dst_smem, const void *map, int x, int y,
-                                                int z, uint32_t cbar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%2, %3, %4}], [%5];"
-        ::"r"(smem_u32(dst_smem)), "l"(map), "r"(x), "r"(y), "r"(z), "r"(cbar)
-        : "memory");
+template <bool PAIR>
+__device__ __forceinline__ void tma_g2s_3d(uint32_t dst, const void *map, int x, int y, int z,
+                                           uint32_t bar) {
+    if constexpr (PAIR)
+        asm volatile(
+            "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::"
+            "bytes [%0], [%1, {%2, %3, %4}], [%5];"
+            ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes "
+            "[%0], [%1, {%2, %3, %4}], [%5];"
+            ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+            : "memory");
 }
 __device__ __forceinline__ void prefetch_tensormap(const void *map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
