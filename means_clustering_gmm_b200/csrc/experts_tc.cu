@@ -98,6 +98,8 @@ template <int KIND, bool GATED, int CG, int W> struct Cfg {
 struct Args {
     ExpCall c;
     CUtensorMap a, b, a2, b2;   // phase 1 and phase 2 operands
+    CUtensorMap aux;            // rows the epilogue reads (dense form)
+    int prefetch_aux;
     int ntn, ntm;               // column tiles; row tiles of one expert's dW
 };
 
@@ -323,6 +325,9 @@ __global__ void __launch_bounds__(kThreads, 1) exp_tc_kernel(const __grid_consta
                 const Job j = job_of<KIND, GATED, CG, W>(a, idx, rank, entry);
                 entry = job_entry<KIND, GATED, CG, W>(a, idx + stride, total);
                 const int row = (int)j.row0;
+                // what the epilogue will read beside the accumulators
+                if (a.prefetch_aux)
+                    for (int i = 0; i < C::NB; i += 64) tma_prefetch_2d(&a.aux, j.col0 + i, row);
                 const int groups = C::kSmallA ? (j.valid + 31) / 32 : 1;
                 const uint32_t bytes_a = C::kSmallA ? groups * (kBytesA / 4) : kBytesA;
                 // this CTA's first column of B in a phase of N columns
@@ -703,6 +708,9 @@ cudaError_t launch_kind(const ExpCall &c, cudaStream_t st) {
             maps.make(&a.b, c.hid, s.h, c.max_rows, 0, kStepK);
             break;
     }
+    const void *aux = KIND == kDaLin ? c.dy : KIND == kSecond || KIND == kFirst ? c.res : nullptr;
+    a.prefetch_aux = s.dense && aux && ((uintptr_t)aux & 15) == 0 && !(KIND == kFirst && s.mlp);
+    if (a.prefetch_aux) maps.make(&a.aux, aux, width, s.N, 0, kRowsA);
     if (!maps.ok) return cudaErrorNotSupported;
     a.ntn = (width + C::NB - 1) / C::NB;
     a.ntm = (mrows + C::kTileRows - 1) / C::kTileRows;

@@ -155,6 +155,12 @@ __device__ __forceinline__ void tma_g2s_3d(uint32_t dst, const void *map, int x,
             ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
             : "memory");
 }
+// A box of a 2-D tensor map on its way into L2; no completion to wait for.
+__device__ __forceinline__ void tma_prefetch_2d(const void *map, int x, int y) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"(map), "r"(x),
+                 "r"(y)
+                 : "memory");
+}
 __device__ __forceinline__ void prefetch_tensormap(const void *map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }

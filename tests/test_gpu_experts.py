@@ -381,13 +381,23 @@ def test_same_expert_twice(N):
     check(s, "silu")
 
 
-def test_result_may_replace_the_residual():
-    for r, N in ((2, 300), (0, 300), (1, 300), (2, 4), (0, 1)):
-        s = inputs(9, N, 64, 72, 64, 3 if r else 1, r, "bf16", res=True)
+@pytest.mark.parametrize("h", [0, 72])
+def test_result_may_replace_the_residual(h):
+    for r, N, o in ((2, 300, 64), (0, 300, 64), (1, 300, 64), (2, 4, 64), (0, 1, 64),
+                    (0, 3000, 520), (1, 9000, 328)):
+        s = inputs(9, N, 64, h, o, 3 if r else 1, r, "bf16", res=True)
         c = cuda(s)
         want = forward(c, "silu")[0]
         got = forward(c, "silu", out=c["res"])[0]
         assert got.data_ptr() == c["res"].data_ptr() and torch.equal(got, want)
+
+
+@pytest.mark.parametrize("r,activation", [(0, "gelu"), (1, "silu")])
+def test_many_tiles_a_block(r, activation):
+    """More tiles than blocks, the last column tile narrower than the others:
+    rows and residuals that are loaded a tile ahead meet their own tile."""
+    s = inputs(21, 12000, 64, 0, 600, 4 if r else 1, r, "f16", res=True, cut=0.2 if r else 0.0)
+    check(s, activation)
 
 
 @pytest.mark.parametrize("N", [5, 400])
