@@ -6,34 +6,149 @@
 
 namespace gmmb {
 
-constexpr int kB = 64, kBK = 16;
+constexpr int kB = 64, kBK = 32;
+
+// Column m of contraction index k sits at m ^ 4 (k / 4 % 8): four indices of a
+// row stored one by one meet 32 banks, and four columns stay together.
+__device__ __forceinline__ int at_col(int k, int m) { return m ^ ((k >> 2 & 7) << 2); }
 
 struct SimtSmem {
-    float a[kBK][kB + 4], b[kBK][kB + 4];
+    float a[2][kBK][kB], b[2][kBK][kB];
 };
 
-// acc[i][j] += sum_k A(ty * 4 + i, k) B(tx * 4 + j, k).  la / lb return one
-// element (0 outside); AK / BK: whether k is the operand's contiguous axis
-// (only the order of the loads depends on it).
-template <bool AK, bool BK, class LA, class LB>
-__device__ __forceinline__ void simt_mma(SimtSmem &sh, float (&acc)[4][4], int64_t K, LA la,
-                                         LB lb) {
-    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-    for (int64_t k0 = 0; k0 < K; k0 += kBK) {
-        __syncthreads();
+// Operands.  KROW: row(m) is the array's row of tile row m (NULL outside),
+// contiguous along the contraction; otherwise row(k) is the row of
+// contraction index k, contiguous along the tile's rows, of which `cols` from
+// column c0 exist.
+template <typename E_> struct GatherRows {   // row tok[m] of [. x ld]
+    using E = E_;
+    static constexpr bool KROW = true;
+    const E *p;
+    const int64_t *tok;
+    int valid, ld;
+    __device__ __forceinline__ const E *row(int m) const {
+        return m < valid ? p + tok[m] * ld : nullptr;
+    }
+};
+template <typename E_> struct PlainRows {    // rows m0 + m of [rows x ld]
+    using E = E_;
+    static constexpr bool KROW = true;
+    const E *p;
+    int m0, rows, ld;
+    __device__ __forceinline__ const E *row(int m) const {
+        return m0 + m < rows ? p + (size_t)(m0 + m) * ld : nullptr;
+    }
+};
+template <typename E_> struct PlainCols {    // columns of rows k of [. x ld]
+    using E = E_;
+    static constexpr bool KROW = false;
+    const E *p;
+    int c0, ld;
+    __device__ __forceinline__ int cols() const { return ld - c0; }
+    __device__ __forceinline__ const E *row(int64_t k) const { return p + k * ld + c0; }
+};
+template <typename E_> struct PointCols {    // columns of the segment's k-th point
+    using E = E_;
+    static constexpr bool KROW = false;
+    const E *p;
+    ExpRoute rt;
+    int64_t row0;
+    int c0, ld;
+    __device__ __forceinline__ int cols() const { return ld - c0; }
+    __device__ __forceinline__ const E *row(int64_t k) const {
+        return p + rt.token(rt.pair(row0 + k)) * ld + c0;
+    }
+};
+
+// A thread's eight elements of a 64 x 32 operand tile, between global and
+// shared memory.  VEC (fp32, rows of whole 16-byte units): two float4.
+template <class OP, bool VEC> struct Part {
+    float r[8];
+    const typename OP::E *p[OP::KROW ? (VEC ? 2 : 8) : 1];
+    __device__ __forceinline__ void begin(const OP &op) {
+        const int tid = threadIdx.x;
+        if constexpr (OP::KROW)
 #pragma unroll
-        for (int i = 0; i < kB * kBK / 256; ++i) {
-            const int e = tid + i * 256;
-            const int ka = AK ? e % kBK : e / kB, m = AK ? e / kBK : e % kB;
-            sh.a[ka][m] = k0 + ka < K ? la(m, k0 + ka) : 0.f;
-            const int kb = BK ? e % kBK : e / kB, n = BK ? e / kBK : e % kB;
-            sh.b[kb][n] = k0 + kb < K ? lb(n, k0 + kb) : 0.f;
+            for (int i = 0; i < (VEC ? 2 : 8); ++i)
+                p[i] = op.row(VEC ? (tid >> 3) + 32 * i : (tid >> 5) + 8 * i);
+    }
+    __device__ __forceinline__ void load(const OP &op, int64_t k0, int64_t K) {
+        const int tid = threadIdx.x;
+#pragma unroll
+        for (int i = 0; i < (VEC ? 2 : 8); ++i) {
+            if constexpr (VEC) {
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                if constexpr (OP::KROW) {
+                    const int64_t k = k0 + (tid & 7) * 4;
+                    if (p[i] && k < K) v = *reinterpret_cast<const float4 *>(p[i] + k);
+                } else {
+                    const int64_t k = k0 + (tid >> 4) + 16 * i;
+                    const int n = (tid & 15) * 4;
+                    if (k < K && n < op.cols())
+                        v = *reinterpret_cast<const float4 *>(op.row(k) + n);
+                }
+                r[4 * i] = v.x;
+                r[4 * i + 1] = v.y;
+                r[4 * i + 2] = v.z;
+                r[4 * i + 3] = v.w;
+            } else if constexpr (OP::KROW) {
+                const int64_t k = k0 + (tid & 31);
+                r[i] = p[i] && k < K ? value_at(p[i] + k) : 0.f;
+            } else {
+                const int64_t k = k0 + (tid >> 6) + 4 * i;
+                const int n = tid & 63;
+                r[i] = k < K && n < op.cols() ? value_at(op.row(k) + n) : 0.f;
+            }
         }
+    }
+    __device__ __forceinline__ void store(float (&sh)[kBK][kB]) const {
+        const int tid = threadIdx.x;
+#pragma unroll
+        for (int i = 0; i < (VEC ? 2 : 8); ++i) {
+            if constexpr (VEC && OP::KROW) {
+                const int k = (tid & 7) * 4, m = (tid >> 3) + 32 * i;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) sh[k + j][at_col(k, m)] = r[4 * i + j];
+            } else if constexpr (VEC) {
+                const int k = (tid >> 4) + 16 * i;
+                *reinterpret_cast<float4 *>(&sh[k][at_col(k, (tid & 15) * 4)]) =
+                    make_float4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+            } else {
+                const int k = OP::KROW ? tid & 31 : (tid >> 6) + 4 * i;
+                const int m = OP::KROW ? (tid >> 5) + 8 * i : tid & 63;
+                sh[k][at_col(k, m)] = r[i];
+            }
+        }
+    }
+};
+
+// acc[i][j] += sum_k A(ty * 4 + i, k) B(tx * 4 + j, k).  The next 32 indices
+// are on their way into registers while these are multiplied, and shared
+// memory is double-buffered: one barrier a step.
+template <bool VEC, class A, class B>
+__device__ __forceinline__ void simt_mma(SimtSmem &sh, float (&acc)[4][4], int64_t K, const A &opa,
+                                         const B &opb) {
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    Part<A, VEC> pa;
+    Part<B, VEC> pb;
+    pa.begin(opa);
+    pb.begin(opb);
+    pa.load(opa, 0, K);
+    pb.load(opb, 0, K);
+    __syncthreads();   // the product before has read both buffers
+    int buf = 0;
+    for (int64_t k0 = 0; k0 < K; k0 += kBK, buf ^= 1) {
+        pa.store(sh.a[buf]);
+        pb.store(sh.b[buf]);
         __syncthreads();
+        if (k0 + kBK < K) {
+            pa.load(opa, k0 + kBK, K);
+            pb.load(opb, k0 + kBK, K);
+        }
 #pragma unroll
         for (int k = 0; k < kBK; ++k) {
-            const float4 av = *reinterpret_cast<const float4 *>(&sh.a[k][ty * 4]);
-            const float4 bv = *reinterpret_cast<const float4 *>(&sh.b[k][tx * 4]);
+            const float4 av = *reinterpret_cast<const float4 *>(&sh.a[buf][k][at_col(k, ty * 4)]);
+            const float4 bv = *reinterpret_cast<const float4 *>(&sh.b[buf][k][at_col(k, tx * 4)]);
             const float a[4] = {av.x, av.y, av.z, av.w}, b[4] = {bv.x, bv.y, bv.z, bv.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -42,53 +157,6 @@ __device__ __forceinline__ void simt_mma(SimtSmem &sh, float (&acc)[4][4], int64
         }
     }
 }
-
-// Operands: one element each, 0 outside.
-template <typename E> struct GatherRows {   // row tok[m] of [. x ld], column k
-    const E *p;
-    const int64_t *tok;
-    int valid, ld;
-    __device__ __forceinline__ float operator()(int m, int64_t k) const {
-        return m < valid ? value_at(p + tok[m] * ld + k) : 0.f;
-    }
-};
-struct OwnRows {   // row m of the block's fp32 rows, column k
-    const float *p;
-    int valid, ld;
-    __device__ __forceinline__ float operator()(int m, int64_t k) const {
-        return m < valid ? p[(int64_t)m * ld + k] : 0.f;
-    }
-};
-template <typename E> struct WeightRows {   // W[n0 + n][k]
-    const E *p;
-    int n0, rows, ld;
-    __device__ __forceinline__ float operator()(int n, int64_t k) const {
-        return n0 + n < rows ? value_at(p + (size_t)(n0 + n) * ld + k) : 0.f;
-    }
-};
-template <typename E> struct WeightCols {   // W[k][n0 + n]
-    const E *p;
-    int n0, ld;
-    __device__ __forceinline__ float operator()(int n, int64_t k) const {
-        return n0 + n < ld ? value_at(p + (size_t)k * ld + n0 + n) : 0.f;
-    }
-};
-template <typename E> struct PointCols {   // column c0 + m of the segment's k-th point
-    const E *p;
-    ExpRoute rt;
-    int64_t row0;
-    int c0, ld;
-    __device__ __forceinline__ float operator()(int m, int64_t k) const {
-        return c0 + m < ld ? value_at(p + rt.token(rt.pair(row0 + k)) * ld + c0 + m) : 0.f;
-    }
-};
-struct OwnCols {   // column c0 + m of the segment's k-th fp32 row
-    const float *p;
-    int c0, ld;
-    __device__ __forceinline__ float operator()(int m, int64_t k) const {
-        return c0 + m < ld ? p[k * ld + c0 + m] : 0.f;
-    }
-};
 
 __device__ __forceinline__ void zero(float (&acc)[4][4]) {
 #pragma unroll
@@ -139,7 +207,7 @@ __device__ __forceinline__ void store_result(const ExpCall &c, int64_t pair, int
 
 // First product: f(W1 x + b1) (gated: f(a) u) to the hidden rows, or, for
 // the linear form, to the result.
-template <typename T, int ACT, bool GATED>
+template <typename T, int ACT, bool GATED, bool V>
 __global__ void __launch_bounds__(256) simt_first_kernel(ExpCall c) {
     __shared__ __align__(16) SimtSmem sh;
     __shared__ int64_t tok[kB], pair[kB];
@@ -157,17 +225,19 @@ __global__ void __launch_bounds__(256) simt_first_kernel(ExpCall c) {
         for (int half = 0; half < (GATED ? 2 : 1); ++half) {
             const T *w = (const T *)c.w1 + ((size_t)rows.expert * c.s.first() +
                                             (size_t)half * width) * d;
-            simt_mma<true, true>(sh, acc[half], d, la, WeightRows<T>{w, n0, width, d});
+            simt_mma<V>(sh, acc[half], d, la, PlainRows<T>{w, n0, width, d});
         }
     }
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const T *b = c.b1 ? (const T *)c.b1 + (size_t)rows.expert * c.s.first() : nullptr;
+#pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int m = ty * 4 + i;
-        if (m >= rows.valid) break;
+        if (m >= rows.valid) continue;
+#pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int col = n0 + tx * 4 + j;
-            if (col >= width) break;
+            if (col >= width) continue;
             float v = 0.f;
             if (!rows.null_expert) {
                 v = act_of<ACT>(acc[0][i][j] + (b ? value_at(b + col) : 0.f));
@@ -182,7 +252,7 @@ __global__ void __launch_bounds__(256) simt_first_kernel(ExpCall c) {
 }
 
 // Second product: W2 h + b2.
-template <typename T>
+template <typename T, bool V>
 __global__ void __launch_bounds__(256) simt_second_kernel(ExpCall c) {
     __shared__ __align__(16) SimtSmem sh;
     __shared__ int64_t tok[kB], pair[kB];
@@ -194,16 +264,18 @@ __global__ void __launch_bounds__(256) simt_second_kernel(ExpCall c) {
     zero(acc);
     if (!rows.null_expert) {
         const T *w = (const T *)c.w2 + (size_t)rows.expert * o * h;
-        simt_mma<true, true>(sh, acc, h, OwnRows{hid + rows.row0 * h, rows.valid, h},
-                             WeightRows<T>{w, n0, o, h});
+        simt_mma<V>(sh, acc, h, PlainRows<float>{hid + rows.row0 * h, 0, rows.valid, h},
+                    PlainRows<T>{w, n0, o, h});
     }
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+#pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int m = ty * 4 + i;
-        if (m >= rows.valid) break;
+        if (m >= rows.valid) continue;
+#pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int col = n0 + tx * 4 + j;
-            if (col >= o) break;
+            if (col >= o) continue;
             float v = acc[i][j];
             if (c.b2 && !rows.null_expert)
                 v += value_at((const T *)c.b2 + (size_t)rows.expert * o + col);
@@ -216,7 +288,7 @@ __global__ void __launch_bounds__(256) simt_second_kernel(ExpCall c) {
 // the hidden gradient (mlp: q = W2^T dy; linear: dy itself), and writes
 // da = d loss / d (W1 x + b1), resp * h for dW2, and this block's part of
 // dresp = <q, h> (mlp) or <dy, f(z)> (linear).
-template <typename T, int ACT, bool GATED>
+template <typename T, int ACT, bool GATED, bool V>
 __global__ void __launch_bounds__(256) simt_da_kernel(ExpCall c) {
     __shared__ __align__(16) SimtSmem sh;
     __shared__ int64_t tok[kB], pair[kB];
@@ -232,25 +304,26 @@ __global__ void __launch_bounds__(256) simt_da_kernel(ExpCall c) {
     for (int half = 0; half < (GATED ? 2 : 1); ++half) {
         const T *w = (const T *)c.w1 + ((size_t)rows.expert * c.s.first() +
                                         (size_t)half * width) * d;
-        simt_mma<true, true>(sh, acc[half], d, GatherRows<T>{x, tok, rows.valid, d},
-                             WeightRows<T>{w, n0, width, d});
+        simt_mma<V>(sh, acc[half], d, GatherRows<T>{x, tok, rows.valid, d},
+                    PlainRows<T>{w, n0, width, d});
     }
     if (c.s.mlp) {
         const T *w = (const T *)c.w2 + (size_t)rows.expert * o * width;
-        simt_mma<true, false>(sh, q, o, GatherRows<T>{dy, tok, rows.valid, o},
-                              WeightCols<T>{w, n0, width});
+        simt_mma<V>(sh, q, o, GatherRows<T>{dy, tok, rows.valid, o}, PlainCols<T>{w, n0, width});
     }
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const T *b = c.b1 ? (const T *)c.b1 + (size_t)rows.expert * c.s.first() : nullptr;
     float *da = (float *)c.da, *hs = (float *)c.hid;
+#pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int m = ty * 4 + i;
         const bool ok = m < rows.valid;
         const int64_t row = rows.row0 + m;
         float part = 0.f;
-        for (int j = 0; j < 4 && ok; ++j) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
             const int col = n0 + tx * 4 + j;
-            if (col >= width) break;
+            if (!ok || col >= width) continue;
             const float g = c.resp ? c.resp[pair[m]] : 1.f;
             float f, df;
             act_both<ACT>(acc[0][i][j] + (b ? value_at(b + col) : 0.f), f, df);
@@ -269,7 +342,7 @@ __global__ void __launch_bounds__(256) simt_da_kernel(ExpCall c) {
 }
 
 // dx (or its per-pair part) = da W1.
-template <typename T>
+template <typename T, bool V>
 __global__ void __launch_bounds__(256) simt_dx_kernel(ExpCall c) {
     __shared__ __align__(16) SimtSmem sh;
     __shared__ int64_t tok[kB], pair[kB];
@@ -281,16 +354,18 @@ __global__ void __launch_bounds__(256) simt_dx_kernel(ExpCall c) {
     zero(acc);
     if (!rows.null_expert) {
         const T *w = (const T *)c.w1 + (size_t)rows.expert * first * d;
-        simt_mma<true, false>(sh, acc, first, OwnRows{da + rows.row0 * first, rows.valid, first},
-                              WeightCols<T>{w, n0, d});
+        simt_mma<V>(sh, acc, first, PlainRows<float>{da + rows.row0 * first, 0, rows.valid, first},
+                    PlainCols<T>{w, n0, d});
     }
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+#pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int m = ty * 4 + i;
-        if (m >= rows.valid) break;
+        if (m >= rows.valid) continue;
+#pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int col = n0 + tx * 4 + j;
-            if (col >= d) break;
+            if (col >= d) continue;
             if (c.s.direct())
                 ((T *)c.dx)[tok[m] * d + col] = from_float<T>(acc[i][j]);
             else
@@ -302,7 +377,7 @@ __global__ void __launch_bounds__(256) simt_dx_kernel(ExpCall c) {
 // Weight gradient of one expert: out[m][n] = sum over its rows of
 // A(row, m) B(row, n).  SECOND: A = dy (gathered), B = resp * h; otherwise
 // A = da, B = x (gathered).
-template <typename T, bool SECOND>
+template <typename T, bool SECOND, bool V>
 __global__ void __launch_bounds__(256) simt_dw_kernel(ExpCall c, int mtiles) {
     __shared__ __align__(16) SimtSmem sh;
     const int e = blockIdx.x / mtiles, m0 = (blockIdx.x % mtiles) * kB, n0 = blockIdx.y * kB;
@@ -315,17 +390,19 @@ __global__ void __launch_bounds__(256) simt_dw_kernel(ExpCall c, int mtiles) {
     float acc[4][4];
     zero(acc);
     const PointCols<T> pc{points, c.rt, row0, SECOND ? m0 : n0, pw};
-    const OwnCols oc{own + row0 * ow, SECOND ? n0 : m0, ow};
-    if (SECOND) simt_mma<false, false>(sh, acc, cnt, pc, oc);
-    else simt_mma<false, false>(sh, acc, cnt, oc, pc);
+    const PlainCols<float> oc{own + row0 * ow, SECOND ? n0 : m0, ow};
+    if constexpr (SECOND) simt_mma<V>(sh, acc, cnt, pc, oc);
+    else simt_mma<V>(sh, acc, cnt, oc, pc);
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     T *out = (T *)(SECOND ? c.dw2 : c.dw1) + (size_t)e * M * N;
+#pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int m = m0 + ty * 4 + i;
-        if (m >= M) break;
+        if (m >= M) continue;
+#pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int n = n0 + tx * 4 + j;
-            if (n >= N) break;
+            if (n >= N) continue;
             out[(size_t)m * N + n] = from_float<T>(acc[i][j]);
         }
     }
@@ -333,26 +410,38 @@ __global__ void __launch_bounds__(256) simt_dw_kernel(ExpCall c, int mtiles) {
 
 static unsigned tiles_of(int64_t n) { return (unsigned)((n + kB - 1) / kB); }
 
-template <typename T, int ACT, bool GATED>
-static void simt_run(const ExpCall &c, bool backward, cudaStream_t s) {
+template <typename T, int ACT, bool GATED, bool V>
+static void simt_products(const ExpCall &c, bool backward, cudaStream_t s) {
     const ExpShape &p = c.s;
     const unsigned rows = 2u * (unsigned)c.rt.max_tiles;
     const int width = p.mlp ? p.h : p.o;
     if (!backward) {
-        simt_first_kernel<T, ACT, GATED><<<dim3(rows, tiles_of(width)), 256, 0, s>>>(c);
-        if (p.mlp) simt_second_kernel<T><<<dim3(rows, tiles_of(p.o)), 256, 0, s>>>(c);
+        simt_first_kernel<T, ACT, GATED, V><<<dim3(rows, tiles_of(width)), 256, 0, s>>>(c);
+        if (p.mlp) simt_second_kernel<T, V><<<dim3(rows, tiles_of(p.o)), 256, 0, s>>>(c);
         note_launches(p.mlp ? 2 : 1);
         return;
     }
-    simt_da_kernel<T, ACT, GATED><<<dim3(rows, tiles_of(width)), 256, 0, s>>>(c);
-    simt_dx_kernel<T><<<dim3(rows, tiles_of(p.d)), 256, 0, s>>>(c);
+    simt_da_kernel<T, ACT, GATED, V><<<dim3(rows, tiles_of(width)), 256, 0, s>>>(c);
+    simt_dx_kernel<T, V><<<dim3(rows, tiles_of(p.d)), 256, 0, s>>>(c);
     const unsigned m1 = tiles_of(p.first());
-    simt_dw_kernel<T, false><<<dim3(m1 * p.K, tiles_of(p.d)), 256, 0, s>>>(c, (int)m1);
+    simt_dw_kernel<T, false, V><<<dim3(m1 * p.K, tiles_of(p.d)), 256, 0, s>>>(c, (int)m1);
     if (p.mlp) {
         const unsigned m2 = tiles_of(p.o);
-        simt_dw_kernel<T, true><<<dim3(m2 * p.K, tiles_of(p.h)), 256, 0, s>>>(c, (int)m2);
+        simt_dw_kernel<T, true, V><<<dim3(m2 * p.K, tiles_of(p.h)), 256, 0, s>>>(c, (int)m2);
     }
     note_launches(p.mlp ? 4 : 3);
+}
+
+template <typename T, int ACT, bool GATED>
+static void simt_run(const ExpCall &c, bool backward, cudaStream_t s) {
+    const ExpShape &p = c.s;
+    // rows of whole 16-byte units in every array that is read along them
+    if constexpr (sizeof(T) == 4)
+        if (p.d % 4 == 0 && p.h % 4 == 0 && (p.o % 4 == 0 || !backward)) {
+            simt_products<T, ACT, GATED, true>(c, backward, s);
+            return;
+        }
+    simt_products<T, ACT, GATED, false>(c, backward, s);
 }
 
 template <typename T, int ACT>
