@@ -86,13 +86,11 @@ Layout layout_of(const ExpShape &p, bool backward, int path) {
     take(L.dyrows, sorted && backward && p.mlp ? (size_t)L.max_rows * p.o * 2 : 0);
     const int wide = !backward ? p.o : (p.d > p.o ? p.d : p.o);
     take(L.slots, p.direct() ? 0 : (size_t)p.P * wide * 4);
-    take(L.rpart, backward ? (size_t)L.max_rows * L.nrpart * 4 : 0);
-    size_t cols = 0;   // partial bias gradients, one bias at a time
-    if (backward && path == 2) {
-        cols = (size_t)exp_colsum_slices(p, p.first()) * p.first();
-        const size_t c2 = (size_t)exp_colsum_slices(p, p.o) * p.o;
-        if (p.mlp && c2 > cols) cols = c2;
-    }
+    take(L.rpart, backward ? (size_t)p.P * L.nrpart * 4 : 0);
+    // partial bias gradients
+    const size_t cols = backward && path == 2
+                            ? (size_t)exp_colsum_slices(p) * (p.first() + (p.mlp ? p.o : 0))
+                            : 0;
     take(L.colpart, cols * p.K * 4);
     L.total = o;
     return L;
@@ -199,7 +197,7 @@ gmm_status forward(const gmm_expert_shape *shape, bool mlp, const void *X, const
     if (path == 1) return launch_exp_few(c, s) == cudaSuccess ? GMM_OK : GMM_ERR_CUDA;
     if (launch_exp_route(c, s) != cudaSuccess) return GMM_ERR_CUDA;
     if (products(c, path, false, s) != cudaSuccess) return GMM_ERR_CUDA;
-    if (!p.direct() && launch_exp_combine(c, false, s) != cudaSuccess) return GMM_ERR_CUDA;
+    if (launch_exp_combine(c, false, s) != cudaSuccess) return GMM_ERR_CUDA;
     return GMM_OK;
 }
 
@@ -251,9 +249,8 @@ gmm_status backward(const gmm_expert_shape *shape, bool mlp, const void *dY, con
     c.dresp = dresp;
     if (launch_exp_route(c, s) != cudaSuccess) return GMM_ERR_CUDA;
     if (products(c, path, true, s) != cudaSuccess) return GMM_ERR_CUDA;
-    if (!p.direct() && launch_exp_combine(c, true, s) != cudaSuccess) return GMM_ERR_CUDA;
+    if (launch_exp_combine(c, true, s) != cudaSuccess) return GMM_ERR_CUDA;
     if (launch_exp_bias_grads(c, s) != cudaSuccess) return GMM_ERR_CUDA;
-    if (dresp && launch_exp_dresp(c, s) != cudaSuccess) return GMM_ERR_CUDA;
     return GMM_OK;
 }
 

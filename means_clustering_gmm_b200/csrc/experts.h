@@ -88,7 +88,7 @@ struct ExpCall {
     int64_t point_rows;
     float *slots, *rpart, *colpart;
     int64_t max_rows;
-    int nrpart;         // partial sums of dresp per row
+    int nrpart;         // partial sums of dresp per pair
     size_t esize;       // bytes per element of hid and da
 };
 
@@ -182,16 +182,40 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(f
     return __float2bfloat16_rn(v);
 }
 
+// Every kernel of a call starts under the tail of the one before it
+// (programmatic dependent launch) and waits here for all of it; what it does
+// before this touches no memory of the call.
+__device__ __forceinline__ void exp_enter() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+template <typename... P, typename... A>
+cudaError_t exp_launch(void (*kernel)(P...), dim3 grid, int block, size_t smem, cudaStream_t s,
+                       const A &...args) {
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    note_launches(1);
+    return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
 // experts_route.cu
 cudaError_t launch_exp_route(const ExpCall &c, cudaStream_t s);
 // the rows of X (and dY) sorted by expert (16-bit types, 16-byte rows)
 cudaError_t launch_exp_gather(const ExpCall &c, bool backward, cudaStream_t s);
-// y_n = sum_i g_ni slots_ni (+ residual_n); dx_n = sum_i slots_ni
+// forward: y_n = sum_i g_ni slots_ni (+ residual_n); backward: dx_n = sum_i
+// slots_ni, and dresp from its partial sums (and <dy, b2>)
 cudaError_t launch_exp_combine(const ExpCall &c, bool backward, cudaStream_t s);
-// dresp from its partial sums (and <dy, b2>); column sums of da and g dy
-cudaError_t launch_exp_dresp(const ExpCall &c, cudaStream_t s);
+// column sums of da and g dy
 cudaError_t launch_exp_bias_grads(const ExpCall &c, cudaStream_t s);
-int exp_colsum_slices(const ExpShape &s, int width);
+int exp_colsum_slices(const ExpShape &s);
 // experts_simt.cu: the products on CUDA cores
 cudaError_t launch_exp_simt(const ExpCall &c, bool backward, cudaStream_t s);
 // experts_tc.cu: on the tensor cores (16-bit types, widths multiples of 8)

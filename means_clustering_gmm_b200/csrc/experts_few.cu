@@ -500,7 +500,7 @@ template <typename T> cudaError_t few_t(const ExpCall &c, cudaStream_t st) {
     }
     if (e != cudaSuccess) return e;
     if (c.s.mlp) return launch_second<T>(c, st);
-    return c.s.direct() ? cudaSuccess : launch_exp_combine(c, false, st);
+    return launch_exp_combine(c, false, st);
 }
 
 }  // namespace

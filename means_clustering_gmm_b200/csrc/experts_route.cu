@@ -22,6 +22,7 @@ __device__ __forceinline__ int pair_key(const int32_t *ids, int64_t p, int K, in
 __global__ void __launch_bounds__(128)
 exp_hist_kernel(ExpRoute rt, int *err) {
     extern __shared__ int sh[];
+    exp_enter();
     const int KK = rt.K + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int *row = sh + warp * KK;
     const int64_t chunk = (int64_t)blockIdx.x * 4 + warp;
@@ -47,6 +48,7 @@ exp_hist_kernel(ExpRoute rt, int *err) {
 // One warp per key: exclusive scan of its counts over the chunks, in place.
 __global__ void __launch_bounds__(128)
 exp_scan_kernel(ExpRoute rt, int64_t nch) {
+    exp_enter();
     const int KK = rt.K + 1, lane = threadIdx.x & 31;
     const int e = blockIdx.x * 4 + (threadIdx.x >> 5);
     if (e >= KK) return;
@@ -146,6 +148,7 @@ __device__ __forceinline__ void make_tiles(const ExpRoute &rt, const int *cnt, i
 __global__ void __launch_bounds__(1024)
 exp_tiles_kernel(ExpRoute rt) {
     extern __shared__ int sh[];
+    exp_enter();
     make_tiles(rt, rt.cnt, sh);
 }
 
@@ -156,6 +159,7 @@ constexpr int kOneBlockKeys = 1024;
 __global__ void __launch_bounds__(1024)
 exp_route_kernel(ExpRoute rt, int *err) {
     extern __shared__ int sh[];
+    exp_enter();
     const int KK = rt.K + 1, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int *counts = sh;                    // [32][KK]
     int *cnt = sh + 32 * KK;             // [KK]
@@ -223,6 +227,7 @@ exp_route_kernel(ExpRoute rt, int *err) {
 __global__ void __launch_bounds__(128)
 exp_scatter_kernel(ExpRoute rt) {
     extern __shared__ int sh[];
+    exp_enter();
     const int KK = rt.K + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int *row = sh + warp * KK;   // next row of each expert for this chunk
     const int64_t chunk = (int64_t)blockIdx.x * 4 + warp;
@@ -262,9 +267,7 @@ cudaError_t launch_exp_route(const ExpCall &c, cudaStream_t s) {
             e = cudaFuncSetAttribute(exp_route_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      bytes);
         if (e != cudaSuccess) return e;
-        exp_route_kernel<<<1, 1024, bytes, s>>>(rt, c.err);
-        note_launches(1);
-        return cudaGetLastError();
+        return exp_launch(exp_route_kernel, dim3(1), 1024, bytes, s, rt, c.err);
     }
     const int64_t nch = (rt.P + kChunkPairs - 1) / kChunkPairs;
     const unsigned blocks = (unsigned)((nch + 3) / 4);
@@ -277,12 +280,12 @@ cudaError_t launch_exp_route(const ExpCall &c, cudaStream_t s) {
                                  smem);
         if (e != cudaSuccess) return e;
     }
-    exp_hist_kernel<<<blocks, 128, smem, s>>>(rt, c.err);
-    exp_scan_kernel<<<(KK + 3) / 4, 128, 0, s>>>(rt, nch);
-    exp_tiles_kernel<<<1, 1024, 2 * (KK + 1) * sizeof(int), s>>>(rt);
-    exp_scatter_kernel<<<blocks, 128, smem, s>>>(rt);
-    note_launches(4);
-    return cudaGetLastError();
+    e = exp_launch(exp_hist_kernel, dim3(blocks), 128, smem, s, rt, c.err);
+    if (e == cudaSuccess) e = exp_launch(exp_scan_kernel, dim3((KK + 3) / 4), 128, 0, s, rt, nch);
+    if (e == cudaSuccess)
+        e = exp_launch(exp_tiles_kernel, dim3(1), 1024, 2 * (KK + 1) * sizeof(int), s, rt);
+    if (e == cudaSuccess) e = exp_launch(exp_scatter_kernel, dim3(blocks), 128, smem, s, rt);
+    return e;
 }
 
 // -------------------------------------------------------------- gather
@@ -292,6 +295,7 @@ cudaError_t launch_exp_route(const ExpCall &c, cudaStream_t s) {
 __global__ void __launch_bounds__(256)
 exp_gather_kernel(ExpRoute rt, const uint4 *__restrict__ x, uint4 *__restrict__ xrows, int xu,
                   const uint4 *__restrict__ dy, uint4 *__restrict__ dyrows, int dyu) {
+    exp_enter();
     const int lane = threadIdx.x & 31;
     const int64_t rows = (int64_t)rt.tiles() * kExpTile;
     const uint4 *src = blockIdx.y ? dy : x;
@@ -322,10 +326,9 @@ cudaError_t launch_exp_gather(const ExpCall &c, bool backward, cudaStream_t s) {
     const int64_t want = (c.max_rows + 7) / 8;
     // (the linear form's gradients read dY through the pairs instead)
     const dim3 grid((unsigned)(want < 148 * 8 ? want : 148 * 8), backward && c.s.mlp ? 2 : 1);
-    exp_gather_kernel<<<grid, 256, 0, s>>>(c.rt, (const uint4 *)c.x, (uint4 *)c.xrows, c.s.d / 8,
-                                           (const uint4 *)c.dy, (uint4 *)c.dyrows, c.s.o / 8);
-    note_launches(1);
-    return cudaGetLastError();
+    return exp_launch(exp_gather_kernel, grid, 256, 0, s, c.rt, (const uint4 *)c.x,
+                      (uint4 *)c.xrows, c.s.d / 8, (const uint4 *)c.dy, (uint4 *)c.dyrows,
+                      c.s.o / 8);
 }
 
 // ------------------------------------------------------------- combine
@@ -333,13 +336,13 @@ cudaError_t launch_exp_gather(const ExpCall &c, bool backward, cudaStream_t s) {
 // bound by HBM.  A thread takes V columns (8: float4 reads, one 16- or
 // 32-byte write; 1: odd widths or a residual that is not 16-byte aligned).
 template <typename T, bool BWD, int V>
-__global__ void __launch_bounds__(256)
-exp_combine_kernel(ExpRoute rt, const float *__restrict__ slots, const float *__restrict__ resp,
-                   const T *res, T *out, int width) {
+__device__ __forceinline__ void combine_rows(const ExpRoute &rt, const float *slots,
+                                             const float *resp, const T *res, T *out, int width,
+                                             int blocks) {
     const int units = width / V;
     const int64_t total = rt.N * units;
     for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < total;
-         i += (int64_t)gridDim.x * 256) {
+         i += (int64_t)blocks * 256) {
         const int64_t n = i / units;
         const int col = (int)(i - n * units) * V;
         float acc[V];
@@ -389,75 +392,64 @@ exp_combine_kernel(ExpRoute rt, const float *__restrict__ slots, const float *__
     }
 }
 
-template <typename T, bool BWD, int V> static void combine_v(const ExpCall &c, cudaStream_t s) {
-    const int width = BWD ? c.s.d : c.s.o;
-    const int64_t want = (c.s.N * (width / V) + 255) / 256;
-    const unsigned grid = (unsigned)(want < 148 * 16 ? want : 148 * 16);
-    exp_combine_kernel<T, BWD, V><<<grid, 256, 0, s>>>(
-        c.rt, c.slots, BWD ? nullptr : c.resp, BWD ? nullptr : (const T *)c.res,
-        (T *)(BWD ? c.dx : c.y), width);
+
+// One warp per pair: its partial sums in order, then <dy, b2>; 0 for an entry
+// without an expert.
+template <typename T>
+__device__ __forceinline__ void dresp_rows(const ExpCall &c, int block, int blocks) {
+    const int lane = threadIdx.x & 31, o = c.s.o;
+    for (int64_t p = block * 8 + (threadIdx.x >> 5); p < c.rt.P; p += blocks * 8) {
+        float acc = 0.f;
+        if (c.rt.used(p)) {
+            for (int i = lane; i < c.nrpart; i += 32) acc += c.rpart[p * c.nrpart + i];
+            if (c.b2) {
+                const T *g = (const T *)c.dy + c.rt.token(p) * o;
+                const T *b = (const T *)c.b2 + (size_t)c.rt.ids[p] * o;
+                for (int i = lane; i < o; i += 32) acc = fmaf(to_float(g[i]), to_float(b[i]), acc);
+            }
+#pragma unroll
+            for (int m = 16; m; m >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, m);
+        }
+        if (lane == 0) c.dresp[p] = acc;
+    }
 }
 
-template <typename T> static void combine_t(const ExpCall &c, bool backward, cudaStream_t s) {
-    if (backward) {
-        if (c.s.d % 8 == 0) combine_v<T, true, 8>(c, s);
-        else combine_v<T, true, 1>(c, s);
-    } else {
-        if (c.s.o % 8 == 0 && ((uintptr_t)c.res & 15) == 0) combine_v<T, false, 8>(c, s);
-        else combine_v<T, false, 1>(c, s);
-    }
+// Blocks below `blocks` sum entries, the others (backward) finish dresp.
+template <typename T, bool BWD, int V>
+__global__ void __launch_bounds__(256) exp_combine_kernel(ExpCall c, int width, int blocks) {
+    exp_enter();
+    if (BWD && (int)blockIdx.x >= blocks)
+        dresp_rows<T>(c, blockIdx.x - blocks, gridDim.x - blocks);
+    else
+        combine_rows<T, BWD, V>(c.rt, c.slots, BWD ? nullptr : c.resp,
+                                BWD ? nullptr : (const T *)c.res, (T *)(BWD ? c.dx : c.y), width,
+                                blocks);
+}
+
+template <typename T, bool BWD, int V>
+static cudaError_t combine_v(const ExpCall &c, cudaStream_t s) {
+    const int width = BWD ? c.s.d : c.s.o;
+    const int64_t want = c.s.direct() ? 0 : (c.s.N * (width / V) + 255) / 256;
+    const int blocks = (int)(want < 148 * 16 ? want : 148 * 16);
+    const int64_t rows = BWD && c.dresp ? (c.s.P + 7) / 8 : 0;
+    const int more = (int)(rows < 148 * 8 ? rows : 148 * 8);
+    return exp_launch(exp_combine_kernel<T, BWD, V>, dim3(blocks + more), 256, 0, s, c, width,
+                      blocks);
+}
+
+template <typename T> static cudaError_t combine_t(const ExpCall &c, bool backward, cudaStream_t s) {
+    if (backward) return c.s.d % 8 == 0 ? combine_v<T, true, 8>(c, s) : combine_v<T, true, 1>(c, s);
+    return c.s.o % 8 == 0 && ((uintptr_t)c.res & 15) == 0 ? combine_v<T, false, 8>(c, s)
+                                                          : combine_v<T, false, 1>(c, s);
 }
 
 cudaError_t launch_exp_combine(const ExpCall &c, bool backward, cudaStream_t s) {
+    if (c.s.direct() && !(backward && c.dresp)) return cudaSuccess;
     switch (c.s.dt) {
-        case GMM_F32: combine_t<float>(c, backward, s); break;
-        case GMM_BF16: combine_t<__nv_bfloat16>(c, backward, s); break;
-        default: combine_t<__half>(c, backward, s);
+        case GMM_F32: return combine_t<float>(c, backward, s);
+        case GMM_BF16: return combine_t<__nv_bfloat16>(c, backward, s);
+        default: return combine_t<__half>(c, backward, s);
     }
-    note_launches(1);
-    return cudaGetLastError();
-}
-
-// --------------------------------------------------------------- dresp
-// One warp per row: the row's partial sums in order, then <dy, b2>.
-template <typename T>
-__global__ void __launch_bounds__(256)
-exp_dresp_kernel(ExpRoute rt, const float *__restrict__ part, int nparts, const T *__restrict__ dy,
-                 const T *__restrict__ b2, int o, float *__restrict__ dresp) {
-    const int lane = threadIdx.x & 31;
-    const int64_t rows = (int64_t)rt.tiles() * kExpTile;
-    for (int64_t row = blockIdx.x * 8 + (threadIdx.x >> 5); row < rows; row += gridDim.x * 8) {
-        const auto t = rt.tile((int)(row / kExpTile));
-        if (row >= t.row0 + t.valid || t.expert >= rt.K) continue;
-        const int64_t p = rt.pair(row);
-        float acc = 0.f;
-        for (int i = lane; i < nparts; i += 32) acc += part[row * nparts + i];
-        if (b2) {
-            const T *g = dy + rt.token(p) * o, *b = b2 + (size_t)t.expert * o;
-            for (int i = lane; i < o; i += 32) acc = fmaf(to_float(g[i]), to_float(b[i]), acc);
-        }
-#pragma unroll
-        for (int m = 16; m; m >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, m);
-        if (lane == 0) dresp[p] = acc;
-    }
-}
-
-template <typename T> static void dresp_t(const ExpCall &c, cudaStream_t s) {
-    exp_dresp_kernel<T><<<148 * 8, 256, 0, s>>>(c.rt, c.rpart, c.nrpart, (const T *)c.dy,
-                                                (const T *)c.b2, c.s.o, c.dresp);
-}
-
-cudaError_t launch_exp_dresp(const ExpCall &c, cudaStream_t s) {
-    // entries without an expert get 0
-    cudaError_t e = cudaMemsetAsync(c.dresp, 0, (size_t)c.s.P * sizeof(float), s);
-    if (e != cudaSuccess) return e;
-    switch (c.s.dt) {
-        case GMM_F32: dresp_t<float>(c, s); break;
-        case GMM_BF16: dresp_t<__nv_bfloat16>(c, s); break;
-        default: dresp_t<__half>(c, s);
-    }
-    note_launches(1);
-    return cudaGetLastError();
 }
 
 // ------------------------------------------------------ bias gradients
@@ -467,6 +459,7 @@ template <typename T, typename E, bool GATHER>
 __global__ void __launch_bounds__(256)
 exp_colsum_kernel(ExpRoute rt, const E *__restrict__ rows, const float *__restrict__ resp,
                   int width, T *__restrict__ out) {
+    exp_enter();
     __shared__ float sh[8][33];
     const int lane = threadIdx.x & 31, ty = threadIdx.x >> 5;
     const int e = blockIdx.y, col = blockIdx.x * 32 + lane;
@@ -491,17 +484,25 @@ exp_colsum_kernel(ExpRoute rt, const E *__restrict__ rows, const float *__restri
     }
 }
 
-// The same over 16-bit rows of whole 16-byte units: 64 columns x 32 row lanes
-// per block, the segment's rows split into S slices (fixed-order partial sums
-// in `part`, added by exp_colsum_join_kernel) when the experts alone make too
-// few blocks.  One dense expert of 8192 x 4096: 94 us unsplit, reading 64 MB.
+// The same over 16-bit rows of whole 16-byte units, for both biases in one
+// launch: 64 columns x 32 row lanes per block, the segment's rows split into S
+// slices (fixed-order partial sums in c.colpart, added by
+// exp_colsum_join_kernel) when the experts alone make too few blocks.  One
+// dense expert of 8192 x 4096 took 94 us unsplit, reading 64 MB; 14 split.
 template <typename T>
 __global__ void __launch_bounds__(256)
-exp_colsum16_kernel(ExpRoute rt, const T *__restrict__ rows, const float *__restrict__ resp,
-                    int width, T *__restrict__ out, float *__restrict__ part) {
+exp_colsum16_kernel(ExpCall c, int w1, int w2) {
     __shared__ float sh[32][65];
-    const int cx = threadIdx.x & 7, ty = threadIdx.x >> 3, S = gridDim.z;
-    const int e = blockIdx.y, col = blockIdx.x * 64 + cx * 8;
+    const ExpRoute &rt = c.rt;
+    const int cx = threadIdx.x & 7, ty = threadIdx.x >> 3, S = gridDim.z, b1 = (w1 + 63) / 64;
+    const bool second = (int)blockIdx.x >= b1;
+    const int width = second ? w2 : w1, c0 = (blockIdx.x - (second ? b1 : 0)) * 64;
+    const int e = blockIdx.y, col = c0 + cx * 8;
+    const T *rows = (const T *)(second ? c.dyrows : c.da);
+    const float *resp = second ? c.resp : nullptr;
+    T *out = (T *)(second ? c.db2 : c.db1);
+    float *part = c.colpart + (second ? (size_t)S * gridDim.y * w1 : 0);
+    exp_enter();
     const int64_t seg = rt.ids ? rt.seg[e] : 0, cnt = rt.ids ? rt.cnt[e] : rt.N;
     const int64_t per = (cnt + S - 1) / S;
     const int64_t beg = seg + blockIdx.z * per;
@@ -522,16 +523,16 @@ exp_colsum16_kernel(ExpRoute rt, const T *__restrict__ rows, const float *__rest
 #pragma unroll
     for (int i = 0; i < 8; ++i) sh[ty][cx * 8 + i] = acc[i];
     __syncthreads();
-    const int c = threadIdx.x & 63, q = threadIdx.x >> 6;   // quarter of the row lanes
+    const int cc = threadIdx.x & 63, q = threadIdx.x >> 6;   // quarter of the row lanes
     float t = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) t += sh[q * 8 + i][c];
+    for (int i = 0; i < 8; ++i) t += sh[q * 8 + i][cc];
     __syncthreads();
-    sh[q][c] = t;
+    sh[q][cc] = t;
     __syncthreads();
-    const int oc = blockIdx.x * 64 + c;
+    const int oc = c0 + cc;
     if (q == 0 && oc < width) {
-        const float v = sh[0][c] + sh[1][c] + sh[2][c] + sh[3][c];
+        const float v = sh[0][cc] + sh[1][cc] + sh[2][cc] + sh[3][cc];
         if (S == 1) out[(size_t)e * width + oc] = from_float<T>(v);
         else part[((size_t)blockIdx.z * gridDim.y + e) * width + oc] = v;
     }
@@ -539,16 +540,22 @@ exp_colsum16_kernel(ExpRoute rt, const T *__restrict__ rows, const float *__rest
 
 template <typename T>
 __global__ void __launch_bounds__(256)
-exp_colsum_join_kernel(const float *__restrict__ part, int S, int64_t n, T *__restrict__ out) {
-    const int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x;
-    if (i >= n) return;
+exp_colsum_join_kernel(ExpCall c, int S, int64_t n1, int64_t n2) {
+    exp_enter();
+    int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x;
+    if (i >= n1 + n2) return;
+    const bool second = i >= n1;
+    const float *part = c.colpart + (second ? S * n1 : 0);
+    if (second) i -= n1;
+    const int64_t n = second ? n2 : n1;
     float t = 0.f;
     for (int k = 0; k < S; ++k) t += part[k * n + i];
-    out[i] = from_float<T>(t);
+    ((T *)(second ? c.db2 : c.db1))[i] = from_float<T>(t);
 }
 
 // Slices of a segment: about four blocks an SM, at least 64 rows a slice.
-int exp_colsum_slices(const ExpShape &s, int width) {
+int exp_colsum_slices(const ExpShape &s) {
+    const int width = s.first() + (s.mlp ? s.o : 0);
     const int64_t blocks = (int64_t)s.K * ((width + 63) / 64);
     int64_t S = (4 * 148 + blocks - 1) / blocks;
     const int64_t most = s.P / s.K / 64;
@@ -556,49 +563,38 @@ int exp_colsum_slices(const ExpShape &s, int width) {
     return (int)(S < 1 ? 1 : S > 32 ? 32 : S);
 }
 
-template <typename T>
-static void colsum16(const ExpCall &c, const void *rows, const float *resp, int width, void *out,
-                     cudaStream_t s) {
-    const int S = exp_colsum_slices(c.s, width);
-    exp_colsum16_kernel<T><<<dim3((width + 63) / 64, c.s.K, S), 256, 0, s>>>(
-        c.rt, (const T *)rows, resp, width, (T *)out, c.colpart);
-    note_launches(1);
-    if (S > 1) {
-        const int64_t n = (int64_t)c.s.K * width;
-        exp_colsum_join_kernel<T><<<(unsigned)((n + 255) / 256), 256, 0, s>>>(c.colpart, S, n,
-                                                                              (T *)out);
-        note_launches(1);
-    }
-}
-
-template <typename T> static void bias_t(const ExpCall &c, cudaStream_t s) {
+template <typename T> static cudaError_t bias_t(const ExpCall &c, cudaStream_t s) {
     const int w = c.s.first();
     if constexpr (sizeof(T) == 2) {
         if (c.esize == 2) {
-            if (c.db1) colsum16<T>(c, c.da, nullptr, w, c.db1, s);
-            if (c.db2) colsum16<T>(c, c.dyrows, c.resp, c.s.o, c.db2, s);
-            return;
+            const int w1 = c.db1 ? w : 0, w2 = c.db2 ? c.s.o : 0, S = exp_colsum_slices(c.s);
+            if (w1 + w2 == 0) return cudaSuccess;
+            cudaError_t e = exp_launch(exp_colsum16_kernel<T>,
+                                       dim3((w1 + 63) / 64 + (w2 + 63) / 64, c.s.K, S), 256, 0, s,
+                                       c, w1, w2);
+            const int64_t n1 = (int64_t)c.s.K * w1, n2 = (int64_t)c.s.K * w2;
+            if (e == cudaSuccess && S > 1)
+                e = exp_launch(exp_colsum_join_kernel<T>, dim3((unsigned)((n1 + n2 + 255) / 256)),
+                               256, 0, s, c, S, n1, n2);
+            return e;
         }
     }
-    if (c.db1) {
-        exp_colsum_kernel<T, float, false><<<dim3((w + 31) / 32, c.s.K), 256, 0, s>>>(
-            c.rt, (const float *)c.da, nullptr, w, (T *)c.db1);
-        note_launches(1);
-    }
-    if (c.db2) {
-        exp_colsum_kernel<T, T, true><<<dim3((c.s.o + 31) / 32, c.s.K), 256, 0, s>>>(
-            c.rt, (const T *)c.dy, c.resp, c.s.o, (T *)c.db2);
-        note_launches(1);
-    }
+    cudaError_t e = cudaSuccess;
+    if (c.db1)
+        e = exp_launch(exp_colsum_kernel<T, float, false>, dim3((w + 31) / 32, c.s.K), 256, 0, s,
+                       c.rt, (const float *)c.da, (const float *)nullptr, w, (T *)c.db1);
+    if (e == cudaSuccess && c.db2)
+        e = exp_launch(exp_colsum_kernel<T, T, true>, dim3((c.s.o + 31) / 32, c.s.K), 256, 0, s,
+                       c.rt, (const T *)c.dy, c.resp, c.s.o, (T *)c.db2);
+    return e;
 }
 
 cudaError_t launch_exp_bias_grads(const ExpCall &c, cudaStream_t s) {
     switch (c.s.dt) {
-        case GMM_F32: bias_t<float>(c, s); break;
-        case GMM_BF16: bias_t<__nv_bfloat16>(c, s); break;
-        default: bias_t<__half>(c, s);
+        case GMM_F32: return bias_t<float>(c, s);
+        case GMM_BF16: return bias_t<__nv_bfloat16>(c, s);
+        default: return bias_t<__half>(c, s);
     }
-    return cudaGetLastError();
 }
 
 }  // namespace gmmb

@@ -212,6 +212,7 @@ __global__ void __launch_bounds__(256) simt_first_kernel(ExpCall c) {
     __shared__ __align__(16) SimtSmem sh;
     __shared__ int64_t tok[kB], pair[kB];
     SimtRows rows;
+    exp_enter();
     if (!rows.load(c.rt, tok, pair)) return;
     const int d = c.s.d, width = c.s.mlp ? c.s.h : c.s.o, n0 = blockIdx.y * kB;
     const T *x = (const T *)c.x;
@@ -257,6 +258,7 @@ __global__ void __launch_bounds__(256) simt_second_kernel(ExpCall c) {
     __shared__ __align__(16) SimtSmem sh;
     __shared__ int64_t tok[kB], pair[kB];
     SimtRows rows;
+    exp_enter();
     if (!rows.load(c.rt, tok, pair)) return;
     const int h = c.s.h, o = c.s.o, n0 = blockIdx.y * kB;
     const float *hid = (const float *)c.hid;
@@ -293,6 +295,7 @@ __global__ void __launch_bounds__(256) simt_da_kernel(ExpCall c) {
     __shared__ __align__(16) SimtSmem sh;
     __shared__ int64_t tok[kB], pair[kB];
     SimtRows rows;
+    exp_enter();
     if (!rows.load(c.rt, tok, pair) || rows.null_expert) return;
     const int d = c.s.d, o = c.s.o, width = c.s.mlp ? c.s.h : c.s.o, n0 = blockIdx.y * kB;
     const T *x = (const T *)c.x, *dy = (const T *)c.dy;
@@ -337,7 +340,7 @@ __global__ void __launch_bounds__(256) simt_da_kernel(ExpCall c) {
         // the 16 lanes of a row
 #pragma unroll
         for (int s = 8; s; s >>= 1) part += __shfl_xor_sync(0xffffffffu, part, s);
-        if (tx == 0 && ok && c.dresp) c.rpart[row * c.nrpart + blockIdx.y] = part;
+        if (tx == 0 && ok && c.dresp) c.rpart[pair[m] * c.nrpart + blockIdx.y] = part;
     }
 }
 
@@ -347,6 +350,7 @@ __global__ void __launch_bounds__(256) simt_dx_kernel(ExpCall c) {
     __shared__ __align__(16) SimtSmem sh;
     __shared__ int64_t tok[kB], pair[kB];
     SimtRows rows;
+    exp_enter();
     if (!rows.load(c.rt, tok, pair)) return;
     const int d = c.s.d, first = c.s.first(), n0 = blockIdx.y * kB;
     const float *da = (const float *)c.da;
@@ -382,6 +386,7 @@ __global__ void __launch_bounds__(256) simt_dw_kernel(ExpCall c, int mtiles) {
     __shared__ __align__(16) SimtSmem sh;
     const int e = blockIdx.x / mtiles, m0 = (blockIdx.x % mtiles) * kB, n0 = blockIdx.y * kB;
     const int M = SECOND ? c.s.o : c.s.first(), N = SECOND ? c.s.h : c.s.d;
+    exp_enter();
     const int64_t row0 = c.rt.ids ? c.rt.seg[e] : 0;
     const int64_t cnt = c.rt.ids ? c.rt.cnt[e] : c.rt.N;
     const float *own = (const float *)(SECOND ? c.hid : c.da);
@@ -411,61 +416,62 @@ __global__ void __launch_bounds__(256) simt_dw_kernel(ExpCall c, int mtiles) {
 static unsigned tiles_of(int64_t n) { return (unsigned)((n + kB - 1) / kB); }
 
 template <typename T, int ACT, bool GATED, bool V>
-static void simt_products(const ExpCall &c, bool backward, cudaStream_t s) {
+static cudaError_t simt_products(const ExpCall &c, bool backward, cudaStream_t s) {
     const ExpShape &p = c.s;
     const unsigned rows = 2u * (unsigned)c.rt.max_tiles;
     const int width = p.mlp ? p.h : p.o;
+    cudaError_t e;
     if (!backward) {
-        simt_first_kernel<T, ACT, GATED, V><<<dim3(rows, tiles_of(width)), 256, 0, s>>>(c);
-        if (p.mlp) simt_second_kernel<T, V><<<dim3(rows, tiles_of(p.o)), 256, 0, s>>>(c);
-        note_launches(p.mlp ? 2 : 1);
-        return;
+        e = exp_launch(simt_first_kernel<T, ACT, GATED, V>, dim3(rows, tiles_of(width)), 256, 0, s,
+                       c);
+        if (e == cudaSuccess && p.mlp)
+            e = exp_launch(simt_second_kernel<T, V>, dim3(rows, tiles_of(p.o)), 256, 0, s, c);
+        return e;
     }
-    simt_da_kernel<T, ACT, GATED, V><<<dim3(rows, tiles_of(width)), 256, 0, s>>>(c);
-    simt_dx_kernel<T, V><<<dim3(rows, tiles_of(p.d)), 256, 0, s>>>(c);
-    const unsigned m1 = tiles_of(p.first());
-    simt_dw_kernel<T, false, V><<<dim3(m1 * p.K, tiles_of(p.d)), 256, 0, s>>>(c, (int)m1);
-    if (p.mlp) {
-        const unsigned m2 = tiles_of(p.o);
-        simt_dw_kernel<T, true, V><<<dim3(m2 * p.K, tiles_of(p.h)), 256, 0, s>>>(c, (int)m2);
-    }
-    note_launches(p.mlp ? 4 : 3);
+    e = exp_launch(simt_da_kernel<T, ACT, GATED, V>, dim3(rows, tiles_of(width)), 256, 0, s, c);
+    if (e == cudaSuccess)
+        e = exp_launch(simt_dx_kernel<T, V>, dim3(rows, tiles_of(p.d)), 256, 0, s, c);
+    const unsigned m1 = tiles_of(p.first()), m2 = tiles_of(p.o);
+    if (e == cudaSuccess)
+        e = exp_launch(simt_dw_kernel<T, false, V>, dim3(m1 * p.K, tiles_of(p.d)), 256, 0, s, c,
+                       (int)m1);
+    if (e == cudaSuccess && p.mlp)
+        e = exp_launch(simt_dw_kernel<T, true, V>, dim3(m2 * p.K, tiles_of(p.h)), 256, 0, s, c,
+                       (int)m2);
+    return e;
 }
 
 template <typename T, int ACT, bool GATED>
-static void simt_run(const ExpCall &c, bool backward, cudaStream_t s) {
+static cudaError_t simt_run(const ExpCall &c, bool backward, cudaStream_t s) {
     const ExpShape &p = c.s;
     // rows of whole 16-byte units in every array that is read along them
     if constexpr (sizeof(T) == 4)
-        if (p.d % 4 == 0 && p.h % 4 == 0 && (p.o % 4 == 0 || !backward)) {
-            simt_products<T, ACT, GATED, true>(c, backward, s);
-            return;
-        }
-    simt_products<T, ACT, GATED, false>(c, backward, s);
+        if (p.d % 4 == 0 && p.h % 4 == 0 && (p.o % 4 == 0 || !backward))
+            return simt_products<T, ACT, GATED, true>(c, backward, s);
+    return simt_products<T, ACT, GATED, false>(c, backward, s);
 }
 
 template <typename T, int ACT>
-static void simt_gate(const ExpCall &c, bool backward, cudaStream_t s) {
-    if (c.s.gated) simt_run<T, ACT, true>(c, backward, s);
-    else simt_run<T, ACT, false>(c, backward, s);
+static cudaError_t simt_gate(const ExpCall &c, bool backward, cudaStream_t s) {
+    return c.s.gated ? simt_run<T, ACT, true>(c, backward, s)
+                     : simt_run<T, ACT, false>(c, backward, s);
 }
 
-template <typename T> static void simt_act(const ExpCall &c, bool backward, cudaStream_t s) {
+template <typename T> static cudaError_t simt_act(const ExpCall &c, bool backward, cudaStream_t s) {
     switch (c.s.act) {
-        case GMM_ACT_RELU: simt_gate<T, GMM_ACT_RELU>(c, backward, s); break;
-        case GMM_ACT_GELU: simt_gate<T, GMM_ACT_GELU>(c, backward, s); break;
-        case GMM_ACT_SILU: simt_gate<T, GMM_ACT_SILU>(c, backward, s); break;
-        default: simt_gate<T, GMM_ACT_NONE>(c, backward, s);
+        case GMM_ACT_RELU: return simt_gate<T, GMM_ACT_RELU>(c, backward, s);
+        case GMM_ACT_GELU: return simt_gate<T, GMM_ACT_GELU>(c, backward, s);
+        case GMM_ACT_SILU: return simt_gate<T, GMM_ACT_SILU>(c, backward, s);
+        default: return simt_gate<T, GMM_ACT_NONE>(c, backward, s);
     }
 }
 
 cudaError_t launch_exp_simt(const ExpCall &c, bool backward, cudaStream_t s) {
     switch (c.s.dt) {
-        case GMM_F32: simt_act<float>(c, backward, s); break;
-        case GMM_BF16: simt_act<__nv_bfloat16>(c, backward, s); break;
-        default: simt_act<__half>(c, backward, s);
+        case GMM_F32: return simt_act<float>(c, backward, s);
+        case GMM_BF16: return simt_act<__nv_bfloat16>(c, backward, s);
+        default: return simt_act<__half>(c, backward, s);
     }
-    return cudaGetLastError();
 }
 
 }  // namespace gmmb

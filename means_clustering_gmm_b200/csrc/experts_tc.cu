@@ -290,6 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1) exp_tc_kernel(const __grid_consta
     else __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    exp_enter();
     const int total = total_jobs<KIND, GATED, CG, W>(a);
 
     if (warp == 0) {
@@ -642,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1) exp_tc_kernel(const __grid_consta
             }
             if constexpr (KIND == kDaLin || KIND == kDaMlp) {
                 if (valid && !none && c.dresp && cw < width)
-                    c.rpart[row * c.nrpart + cw / kPart] = part;
+                    c.rpart[pair * c.nrpart + cw / kPart] = part;
             }
             tc_fence_before();
             __syncwarp();
@@ -720,16 +721,19 @@ cudaError_t launch_kind(const ExpCall &c, cudaStream_t st) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)C::kSmem);
     if (e != cudaSuccess) return e;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = C::kSmem;
     cfg.stream = st;
     cfg.attrs = attr;
+    cfg.numAttrs = 1;
     if (CG == 2) {
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim = {2, 1, 1};
-        cfg.numAttrs = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim = {2, 1, 1};
+        cfg.numAttrs = 2;
     }
     // one wave: as many pairs as can be resident (a GPC with an odd number of
     // SMs leaves one out)
