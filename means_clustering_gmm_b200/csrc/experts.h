@@ -185,8 +185,11 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(f
 // Every kernel of a call starts under the tail of the one before it
 // (programmatic dependent launch) and waits here for all of it; what it does
 // before this touches no memory of the call.
-__device__ __forceinline__ void exp_enter() {
+__device__ __forceinline__ void exp_wait() {
     asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void exp_enter() {
+    exp_wait();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 template <typename... P, typename... A>

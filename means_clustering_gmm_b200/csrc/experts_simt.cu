@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(256) simt_first_kernel(ExpCall c) {
     __shared__ __align__(16) SimtSmem sh;
     __shared__ int64_t tok[kB], pair[kB];
     SimtRows rows;
-    exp_enter();
+    exp_wait();
     if (!rows.load(c.rt, tok, pair)) return;
     const int d = c.s.d, width = c.s.mlp ? c.s.h : c.s.o, n0 = blockIdx.y * kB;
     const T *x = (const T *)c.x;
@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(256) simt_second_kernel(ExpCall c) {
     __shared__ __align__(16) SimtSmem sh;
     __shared__ int64_t tok[kB], pair[kB];
     SimtRows rows;
-    exp_enter();
+    exp_wait();
     if (!rows.load(c.rt, tok, pair)) return;
     const int h = c.s.h, o = c.s.o, n0 = blockIdx.y * kB;
     const float *hid = (const float *)c.hid;
@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(256) simt_da_kernel(ExpCall c) {
     __shared__ __align__(16) SimtSmem sh;
     __shared__ int64_t tok[kB], pair[kB];
     SimtRows rows;
-    exp_enter();
+    exp_wait();
     if (!rows.load(c.rt, tok, pair) || rows.null_expert) return;
     const int d = c.s.d, o = c.s.o, width = c.s.mlp ? c.s.h : c.s.o, n0 = blockIdx.y * kB;
     const T *x = (const T *)c.x, *dy = (const T *)c.dy;
@@ -350,7 +350,7 @@ __global__ void __launch_bounds__(256) simt_dx_kernel(ExpCall c) {
     __shared__ __align__(16) SimtSmem sh;
     __shared__ int64_t tok[kB], pair[kB];
     SimtRows rows;
-    exp_enter();
+    exp_wait();
     if (!rows.load(c.rt, tok, pair)) return;
     const int d = c.s.d, first = c.s.first(), n0 = blockIdx.y * kB;
     const float *da = (const float *)c.da;
@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(256) simt_dw_kernel(ExpCall c, int mtiles) {
     __shared__ __align__(16) SimtSmem sh;
     const int e = blockIdx.x / mtiles, m0 = (blockIdx.x % mtiles) * kB, n0 = blockIdx.y * kB;
     const int M = SECOND ? c.s.o : c.s.first(), N = SECOND ? c.s.h : c.s.d;
-    exp_enter();
+    exp_wait();
     const int64_t row0 = c.rt.ids ? c.rt.seg[e] : 0;
     const int64_t cnt = c.rt.ids ? c.rt.cnt[e] : c.rt.N;
     const float *own = (const float *)(SECOND ? c.hid : c.da);
