@@ -416,11 +416,12 @@ gmm_status kmeans_step(const void *X, gmm_dtype dtype, int B, int64_t N, int d, 
  * sum has a fixed order: results are bitwise reproducible.
  *
  * The kernels, by sizes and types (gmm_expert_path):
- *   2  16-bit types, d, h and o multiples of 8, X, dY and weights 16-byte
- *      aligned: grouped products on the tensor cores (tcgen05);
- *   1  the same with at most 64 points and GMM_EXPERT_FEW_PAIRS pairs, forward
- *      only: kernels that stream each used expert's weights once;
- *   0  everything else (fp32, odd sizes) and GMM_FLAG_FORCE_SIMT: CUDA cores.
+ *   2  16-bit types: grouped products on the tensor cores (tcgen05); where d,
+ *      h or o is not a multiple of 8, on zero-padded copies in the workspace;
+ *   1  16-bit types, d, h and o multiples of 8, at most 64 points and
+ *      GMM_EXPERT_FEW_PAIRS pairs, forward only: kernels that stream each used
+ *      expert's weights once;
+ *   0  fp32, and GMM_FLAG_FORCE_SIMT: CUDA cores.
  */
 typedef enum gmm_activation {
     GMM_ACT_NONE = 0,

@@ -41,21 +41,35 @@ ExpShape make_shape(const gmm_expert_shape *s) {
     return p;
 }
 
+// Tensor maps want rows of whole 16-byte units: other widths run on copies.
+int up8(int w) { return (w + 7) / 8 * 8; }
+bool padded(const ExpShape &p, int path) {
+    return path == 2 && (p.d % 8 || p.h % 8 || p.o % 8);
+}
+ExpShape pad_shape(ExpShape p) {
+    p.d = up8(p.d);
+    p.h = up8(p.h);
+    p.o = up8(p.o);
+    p.gh = p.gated ? 2 * p.h : p.h;
+    return p;
+}
+
 int path_of(const ExpShape &p, bool backward, uint32_t flags) {
-    if (flags & GMM_FLAG_FORCE_SIMT) return 0;
-    // tensor maps want rows of whole 16-byte units
-    if (p.dt == GMM_F32 || p.d % 8 || p.h % 8 || p.o % 8) return 0;
-    if (!backward && p.N <= kExpFewPoints && p.P <= GMM_EXPERT_FEW_PAIRS) return 1;
+    if ((flags & GMM_FLAG_FORCE_SIMT) || p.dt == GMM_F32) return 0;
+    if (!padded(p, 2) && !backward && p.N <= kExpFewPoints && p.P <= GMM_EXPERT_FEW_PAIRS)
+        return 1;
     return 2;
 }
 
 struct Layout {
-    size_t cnt, seg, tile_at, pair_at, ntiles, row_pair, hist, hid, da, xrows, dyrows, slots, rpart, colpart, total;
+    size_t cnt, seg, tile_at, pair_at, ntiles, row_pair, hist, hid, da, xrows, dyrows, slots,
+        rpart, colpart, total;
     int64_t max_rows;
     int max_tiles, nrpart;
     size_t esize;
 };
 
+// `p`: the padded shape where the call runs on copies.
 Layout layout_of(const ExpShape &p, bool backward, int path) {
     Layout L;
     const int64_t segs = p.dense ? 1 : (p.K + 1 < p.P ? p.K + 1 : p.P);
@@ -151,17 +165,86 @@ struct Checks {
     }
 };
 
-// The products of one call, after its routing.
-cudaError_t products(ExpCall &c, int path, bool backward, cudaStream_t s) {
-    if (path == 0) return launch_exp_simt(c, backward, s);
-    if (c.s.dense) {
-        c.xrows = const_cast<void *>(c.x);
-        c.dyrows = const_cast<void *>(c.dy);
-    } else {
-        const cudaError_t e = launch_exp_gather(c, backward, s);
-        if (e != cudaSuccess) return e;
+// The padded copies of a call's arrays, at the end of its workspace.  take()
+// gives an input its copy, give() an output its padded form; both leave arrays
+// alone whose own widths need nothing.
+struct Pads {
+    bool on;
+    size_t o;       // offset past what is taken
+    char *ws;       // NULL: only sizes are wanted
+    PadJobs in, out;
+    Pads(bool on_, size_t base, void *w) : on(on_), o(base), ws((char *)w), in(), out() {}
+    void *job(PadJobs &list, const void *a, int planes, int rows, int cols, int rows_to,
+              int cols_to, int per_expert) {
+        if (!on || (rows == rows_to && cols == cols_to)) return const_cast<void *>(a);
+        void *wide = ws + o;
+        o = align_up(o + (size_t)planes * rows_to * cols_to * 2);
+        if (!ws || !a) return nullptr;
+        list.j[list.n++] = PadJob{const_cast<void *>(a), wide, planes, rows, cols, rows_to,
+                                  cols_to, per_expert};
+        return wide;
     }
-    return launch_exp_tc(c, backward, s);
+    // every array of a call, in `c` on entry as the caller gave it
+    void arrays(ExpCall &c, const ExpShape &p, bool backward) {
+        const int n = (int)p.N, dp = up8(p.d), hp = up8(p.h), op = up8(p.o);
+        const int half = p.gated ? 2 : 1;   // W1's blocks of rows per expert
+        const int r1 = p.mlp ? p.h : p.o, r1p = p.mlp ? hp : op;
+        c.x = job(in, c.x, 1, n, p.d, n, dp, 0);
+        c.w1 = job(in, c.w1, p.K * half, r1, p.d, r1p, dp, half);
+        c.b1 = job(in, c.b1, p.K * half, 1, r1, 1, r1p, half);
+        if (p.mlp) {
+            c.w2 = job(in, c.w2, p.K, p.o, p.h, op, hp, 1);
+            c.b2 = job(in, c.b2, p.K, 1, p.o, 1, op, 1);
+        }
+        if (!backward) {
+            c.res = job(in, c.res, 1, n, p.o, n, op, 0);
+            c.y = job(out, c.y, 1, n, p.o, n, op, 0);
+            return;
+        }
+        c.dy = job(in, c.dy, 1, n, p.o, n, op, 0);
+        c.dx = job(out, c.dx, 1, n, p.d, n, dp, 0);
+        c.dw1 = job(out, c.dw1, p.K * half, r1, p.d, r1p, dp, half);
+        c.db1 = job(out, c.db1, p.K * half, 1, r1, 1, r1p, half);
+        if (p.mlp) {
+            c.dw2 = job(out, c.dw2, p.K, p.o, p.h, op, hp, 1);
+            c.db2 = job(out, c.db2, p.K, 1, p.o, 1, op, 1);
+        }
+    }
+};
+
+size_t total_bytes(const ExpShape &p, bool backward, uint32_t flags) {
+    const int path = path_of(p, backward, flags);
+    const bool on = padded(p, path);
+    Pads pads(on, layout_of(on ? pad_shape(p) : p, backward, path).total, nullptr);
+    ExpCall c = {};
+    pads.arrays(c, p, backward);
+    return pads.o;
+}
+
+// One checked call: routing, copies, products, the sums after them.
+gmm_status run(ExpCall &c, const ExpShape &p, const Layout &L, int path, bool backward, void *ws,
+               cudaStream_t s) {
+    if (path == 1) return launch_exp_few(c, s) == cudaSuccess ? GMM_OK : GMM_ERR_CUDA;
+    Pads pads(padded(p, path), L.total, ws);
+    pads.arrays(c, p, backward);
+    pads.in.cnt = p.dense ? nullptr : c.rt.cnt;
+    cudaError_t e = launch_exp_route(c, s);
+    if (e == cudaSuccess) e = launch_exp_pad(pads.in, false, s);
+    if (path == 0) {
+        if (e == cudaSuccess) e = launch_exp_simt(c, backward, s);
+    } else {
+        if (c.s.dense) {
+            c.xrows = const_cast<void *>(c.x);
+            c.dyrows = const_cast<void *>(c.dy);
+        } else if (e == cudaSuccess) {
+            e = launch_exp_gather(c, backward, s);
+        }
+        if (e == cudaSuccess) e = launch_exp_tc(c, backward, s);
+    }
+    if (e == cudaSuccess) e = launch_exp_combine(c, backward, s);
+    if (e == cudaSuccess && backward) e = launch_exp_bias_grads(c, s);
+    if (e == cudaSuccess) e = launch_exp_pad(pads.out, true, s);
+    return e == cudaSuccess ? GMM_OK : GMM_ERR_CUDA;
 }
 
 gmm_status forward(const gmm_expert_shape *shape, bool mlp, const void *X, const int32_t *ids,
@@ -171,7 +254,8 @@ gmm_status forward(const gmm_expert_shape *shape, bool mlp, const void *X, const
     if (!valid_shape(shape, mlp) || !known_flags(flags)) return GMM_ERR_INVALID_ARG;
     const ExpShape p = make_shape(shape);
     const int path = path_of(p, false, flags);
-    const Layout L = layout_of(p, false, path);
+    const ExpShape q = padded(p, path) ? pad_shape(p) : p;
+    const Layout L = layout_of(q, false, path);
     Checks k;
     k.elem = p.dt == GMM_F32 ? 4 : 2;
     k.big(X);
@@ -183,9 +267,9 @@ gmm_status forward(const gmm_expert_shape *shape, bool mlp, const void *X, const
     k.small(residual, k.elem);
     k.routing(shape, ids, resp);
     k.ok = k.ok && Y != X;
-    k.workspace(ws, ws_bytes, L.total);
+    k.workspace(ws, ws_bytes, total_bytes(p, false, flags));
     if (!k.ok) return GMM_ERR_INVALID_ARG;
-    ExpCall c = make_call(p, L, ws, ids);
+    ExpCall c = make_call(q, L, ws, ids);
     c.x = X;
     c.w1 = W1;
     c.b1 = b1;
@@ -194,11 +278,7 @@ gmm_status forward(const gmm_expert_shape *shape, bool mlp, const void *X, const
     c.res = residual;
     c.resp = resp;
     c.y = Y;
-    if (path == 1) return launch_exp_few(c, s) == cudaSuccess ? GMM_OK : GMM_ERR_CUDA;
-    if (launch_exp_route(c, s) != cudaSuccess) return GMM_ERR_CUDA;
-    if (products(c, path, false, s) != cudaSuccess) return GMM_ERR_CUDA;
-    if (launch_exp_combine(c, false, s) != cudaSuccess) return GMM_ERR_CUDA;
-    return GMM_OK;
+    return run(c, p, L, path, false, ws, s);
 }
 
 gmm_status backward(const gmm_expert_shape *shape, bool mlp, const void *dY, const void *X,
@@ -209,7 +289,8 @@ gmm_status backward(const gmm_expert_shape *shape, bool mlp, const void *dY, con
     if (!valid_shape(shape, mlp) || !known_flags(flags)) return GMM_ERR_INVALID_ARG;
     const ExpShape p = make_shape(shape);
     const int path = path_of(p, true, flags);
-    const Layout L = layout_of(p, true, path);
+    const ExpShape q = padded(p, path) ? pad_shape(p) : p;
+    const Layout L = layout_of(q, true, path);
     Checks k;
     k.elem = p.dt == GMM_F32 ? 4 : 2;
     k.big(dY);
@@ -231,9 +312,9 @@ gmm_status backward(const gmm_expert_shape *shape, bool mlp, const void *dY, con
     k.pair(resp, dresp);
     k.routing(shape, ids, resp);
     k.ok = k.ok && dX != X && dX != dY;
-    k.workspace(ws, ws_bytes, L.total);
+    k.workspace(ws, ws_bytes, total_bytes(p, true, flags));
     if (!k.ok) return GMM_ERR_INVALID_ARG;
-    ExpCall c = make_call(p, L, ws, ids);
+    ExpCall c = make_call(q, L, ws, ids);
     c.dy = dY;
     c.x = X;
     c.w1 = W1;
@@ -247,11 +328,7 @@ gmm_status backward(const gmm_expert_shape *shape, bool mlp, const void *dY, con
     c.dw2 = dW2;
     c.db2 = db2;
     c.dresp = dresp;
-    if (launch_exp_route(c, s) != cudaSuccess) return GMM_ERR_CUDA;
-    if (products(c, path, true, s) != cudaSuccess) return GMM_ERR_CUDA;
-    if (launch_exp_combine(c, true, s) != cudaSuccess) return GMM_ERR_CUDA;
-    if (launch_exp_bias_grads(c, s) != cudaSuccess) return GMM_ERR_CUDA;
-    return GMM_OK;
+    return run(c, p, L, path, true, ws, s);
 }
 
 }  // namespace
@@ -267,9 +344,9 @@ size_t gmm_expert_workspace_size(const gmm_expert_shape *shape, int backward_cal
                                  uint32_t flags) {
     if (!shape || !valid_shape(shape, shape->h > 0) || !known_flags(flags)) return 0;
     const ExpShape p = make_shape(shape);
-    const size_t fwd = layout_of(p, false, path_of(p, false, flags)).total;
+    const size_t fwd = total_bytes(p, false, flags);
     if (!backward_call) return fwd;
-    const size_t bwd = layout_of(p, true, path_of(p, true, flags)).total;
+    const size_t bwd = total_bytes(p, true, flags);
     return bwd > fwd ? bwd : fwd;
 }
 

@@ -219,6 +219,19 @@ cudaError_t launch_exp_combine(const ExpCall &c, bool backward, cudaStream_t s);
 // column sums of da and g dy
 cudaError_t launch_exp_bias_grads(const ExpCall &c, cudaStream_t s);
 int exp_colsum_slices(const ExpShape &s);
+// experts_pad.cu: copies between [planes x rows x cols] and its zero-padded
+// form [planes x rows_to x cols_to] (16-bit elements, cols_to a multiple of 8)
+struct PadJob {
+    void *narrow, *wide;
+    int planes, rows, cols, rows_to, cols_to;
+    int per_expert;   // planes of an expert: planes of unused ones are left; 0: all
+};
+struct PadJobs {
+    PadJob j[8];
+    int n;
+    const int *cnt;   // rows of each expert, NULL: all are used
+};
+cudaError_t launch_exp_pad(const PadJobs &jobs, bool back, cudaStream_t s);
 // experts_simt.cu: the products on CUDA cores
 cudaError_t launch_exp_simt(const ExpCall &c, bool backward, cudaStream_t s);
 // experts_tc.cu: on the tensor cores (16-bit types, widths multiples of 8)

@@ -46,6 +46,8 @@ def test_sizes_and_flags():
     # 16-bit operands for the tensor cores, fp32 ones for the CUDA cores
     big = shape(N=10000, h=1024, d=512, o=512)
     assert size(big, 1) < size(big, 1, _lib.GMM_FLAG_FORCE_SIMT)
+    # copies where a width is not a multiple of 8
+    assert size(shape(d=63)) > size(shape()) and size(shape(o=31), 1) > size(shape(), 1)
     # nothing of size N x K x width: rows grow with the pairs
     assert size(shape(N=100000, h=64, K=64), 1) < 2 * size(shape(N=100000, h=64, K=4), 1)
     assert _lib.load().gmm_expert_workspace_size(None, 0, 0) == 0
@@ -122,6 +124,7 @@ def test_binding_refuses_on_the_host():
     assert gmm.expert_path(64, 8, 16, 8, 9, 5) == 2       # more pairs
     assert gmm.expert_path(65, 8, 16, 8, 9, 1) == 2       # more points
     assert gmm.expert_path(1, 8, 16, 8, 9, 1, backward=True) == 2
-    assert gmm.expert_path(100, 7, 0, 8, 2, 1) == 0
+    assert gmm.expert_path(100, 7, 0, 8, 2, 1) == 2       # on padded copies
+    assert gmm.expert_path(5, 7, 0, 8, 2, 1) == 2
     assert gmm.expert_path(100, 8, 0, 8, 2, 1, torch.float32) == 0
     assert gmm.expert_path(100, 8, 0, 8, 2, 1, flags=gmm.GMM_FLAG_FORCE_SIMT) == 0

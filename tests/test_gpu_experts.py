@@ -277,6 +277,11 @@ MLP = [
     (400, 128, 320, 128, 16, 2, "bf16", "silu", True, {}),
     (300, 64, 64, 64, 64, 8, "f16", "gelu", False, {"bias": False}),
     (150, 50, 60, 70, 6, 3, "f32", "gelu", True, {"cut": 0.2}),
+    (150, 50, 60, 70, 6, 3, "bf16", "gelu", True, {"cut": 0.2, "res": True}),   # padded copies:
+    (700, 64, 61, 64, 2, 2, "f16", "silu", True, {}),                           # h alone
+    (90, 63, 64, 64, 40, 1, "bf16", "silu", False, {"resp": False}),            # d alone
+    (200, 8, 16, 9, 1, 0, "f16", "gelu", False, {"res": True}),                 # o alone, dense
+    (1, 7, 5, 3, 4, 2, "bf16", "silu", True, {"bias": False}),
     (600, 64, 72, 64, 200, 2, "bf16", "none", False, {"use": [3, 198, 199], "resp": False}),
     (1000, 72, 136, 200, 2, 2, "bf16", "silu", True, {"cut": 0.1, "res": True}),   # pairs of tiles
     (700, 200, 264, 72, 2, 2, "f16", "gelu", False, {}),
