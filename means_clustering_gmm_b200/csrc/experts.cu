@@ -85,7 +85,7 @@ Layout layout_of(const ExpShape &p, bool backward, int path) {
         o = align_up(o + bytes);
     };
     const size_t KK = (size_t)p.K + 1;
-    const size_t chunks = p.dense ? 0 : (size_t)((p.P + 255) / 256);
+    const size_t chunks = p.dense ? 0 : (size_t)((p.P + kExpChunk - 1) / kExpChunk);
     take(L.cnt, p.dense ? 0 : KK * 4);
     take(L.seg, p.dense ? 0 : (KK + 1) * 4);
     take(L.tile_at, p.dense ? 0 : (size_t)L.max_tiles * 16);

@@ -11,6 +11,8 @@ namespace gmmb {
 // Rows of one expert's segment start at a multiple of kExpTile, so that a
 // tile of rows belongs to one expert.
 constexpr int kExpTile = 128;
+// Pairs per histogram of the routing's sort.
+constexpr int kExpChunk = 64;
 
 struct ExpShape {
     int64_t N, P;   // points; (point, entry) pairs, N * max(r, 1)

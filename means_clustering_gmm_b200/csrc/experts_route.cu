@@ -1,7 +1,7 @@
 // Routing of the experts' products and the sums around them.
 //
 // Routing is a stable counting sort of the (point, entry) pairs by expert,
-// as the k-means update sorts points by cluster: histograms of chunks of 256
+// as the k-means update sorts points by cluster: histograms of chunks of 64
 // pairs (one warp each), a scan over the chunks per expert, a scan over the
 // experts with every segment rounded up to whole 128-row tiles, a stable
 // scatter.  No floating-point atomics and no order that depends on
@@ -10,7 +10,7 @@
 
 namespace gmmb {
 
-constexpr int kChunkPairs = 256;   // pairs per warp of the sort
+constexpr int kChunkPairs = kExpChunk;   // pairs per warp of the sort
 
 // Key of a pair: its expert, or K where it has none.
 __device__ __forceinline__ int pair_key(const int32_t *ids, int64_t p, int K, int *err) {
@@ -289,9 +289,9 @@ cudaError_t launch_exp_route(const ExpCall &c, cudaStream_t s) {
 }
 
 // -------------------------------------------------------------- gather
-// One warp per row of a segment's tiles: a copy of its point's row, zeros
-// past the segment (the weight gradients contract over whole tiles).  Bound
-// by HBM.
+// The rows of the segments' tiles: copies of their points' rows, zeros past a
+// segment (the weight gradients contract over whole tiles).  A warp takes four
+// rows at once, so that their loads are under way together; bound by HBM.
 __global__ void __launch_bounds__(256)
 exp_gather_kernel(ExpRoute rt, const uint4 *__restrict__ x, uint4 *__restrict__ xrows, int xu,
                   const uint4 *__restrict__ dy, uint4 *__restrict__ dyrows, int dyu) {
@@ -301,29 +301,27 @@ exp_gather_kernel(ExpRoute rt, const uint4 *__restrict__ x, uint4 *__restrict__ 
     const uint4 *src = blockIdx.y ? dy : x;
     uint4 *dst = blockIdx.y ? dyrows : xrows;
     const int u = blockIdx.y ? dyu : xu;
-    for (int64_t row = blockIdx.x * 8 + (threadIdx.x >> 5); row < rows; row += gridDim.x * 8) {
+    for (int64_t row = (blockIdx.x * 8 + (threadIdx.x >> 5)) * 4; row < rows;
+         row += gridDim.x * 32) {
+        const int4 p4 = *reinterpret_cast<const int4 *>(rt.row_pair + row);
+        const int pairs[4] = {p4.x, p4.y, p4.z, p4.w};
         const auto t = rt.tile((int)(row / kExpTile));
-        if (t.expert >= rt.K) continue;
-        uint4 *o = dst + row * u;
-        if (row < t.row0 + t.valid) {
-            const uint4 *p = src + rt.token(rt.pair(row)) * u;
-            int i = lane;
-            for (; i + 96 < u; i += 128) {
-                const uint4 a = p[i], b = p[i + 32], c = p[i + 64], d = p[i + 96];
-                o[i] = a;
-                o[i + 32] = b;
-                o[i + 64] = c;
-                o[i + 96] = d;
-            }
-            for (; i < u; i += 32) o[i] = p[i];
-        } else {
-            for (int i = lane; i < u; i += 32) o[i] = make_uint4(0u, 0u, 0u, 0u);
+        const int left = (int)(t.row0 + t.valid - row);   // rows of the segment from here
+        const uint4 *p[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) p[k] = k < left ? src + rt.token(pairs[k]) * u : nullptr;
+        for (int i = lane; i < u; i += 32) {
+            uint4 v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = p[k] ? p[k][i] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) dst[(row + k) * u + i] = v[k];
         }
     }
 }
 
 cudaError_t launch_exp_gather(const ExpCall &c, bool backward, cudaStream_t s) {
-    const int64_t want = (c.max_rows + 7) / 8;
+    const int64_t want = (c.max_rows + 31) / 32;
     // (the linear form's gradients read dY through the pairs instead)
     const dim3 grid((unsigned)(want < 148 * 8 ? want : 148 * 8), backward && c.s.mlp ? 2 : 1);
     return exp_launch(exp_gather_kernel, grid, 256, 0, s, c.rt, (const uint4 *)c.x,

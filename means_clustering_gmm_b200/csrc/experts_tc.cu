@@ -63,12 +63,12 @@ enum Kind {
 // Gated, those take the other 256 columns, once: the next tile's phase 1
 // covers the epilogue.  Otherwise they are double-buffered too.
 //
-// W: columns of the other kinds' tiles, 128 where the result has no more.
+// W: weight rows (or columns) of the other kinds' tiles.
 template <int KIND, bool GATED, int CG, int W> struct Cfg {
     static constexpr bool kGrad = KIND == kDw1 || KIND == kDw2;
     static constexpr bool kTwo = KIND == kDaMlp;
-    static constexpr int NB = kTwo || (KIND == kFirst && GATED) ? 128 : W;
-    static constexpr int N1 = kTwo ? 128 : KIND == kFirst && GATED ? 256 : W;
+    static constexpr int NB = kTwo ? 128 : GATED ? W / 2 : W;
+    static constexpr int N1 = kTwo ? 128 : W;
     static constexpr int N2 = kTwo ? (GATED ? 256 : 128) : 0;
     static constexpr int kB1 = N1 / CG * kStepK * 2, kB2 = N2 / CG * kStepK * 2;
     static constexpr int kBytesB = kB1 > kB2 ? kB1 : kB2;
@@ -516,6 +516,15 @@ __global__ void __launch_bounds__(kThreads, 1) exp_tc_kernel(const __grid_consta
                     load16(aux + col, col + 8 < width, aux_wide, aux_vec, next);
             };
             if (with_aux) fetch(cw);
+            // and the next job's part of it (one 128-byte line a row) for L2:
+            // points' rows are scattered
+            int64_t next_pair = -1;
+            int next_col = 0;
+            if (with_aux && !s.dense && idx + stride < total) {
+                const Job jn = job_of<KIND, GATED, CG, W>(a, idx + stride, rank, entry);
+                next_col = jn.col0 + pt * kPart;
+                if (m < jn.valid && next_col < width) next_pair = rt.pair(jn.row0 + m);
+            }
             __syncwarp();
             if (!__all_sync(0xffffffffu, mbar_wait(&bars->accfull[buf], (tile >> 1) & 1, c.err,
                                                    abort_flag)))
@@ -524,6 +533,10 @@ __global__ void __launch_bounds__(kThreads, 1) exp_tc_kernel(const __grid_consta
             // column 0 of the (last phase's) accumulator, and q's
             const uint32_t acc = tmem + (C::kTwo ? C::col2(tile) : C::col1(tile)) + lane_base;
             const uint32_t accq = tmem + C::col1(tile) + lane_base;
+            if (next_pair >= 0)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"((const T *)aux0 +
+                                                              rt.token(next_pair) * width +
+                                                              next_col));
             const bool has = j.steps1 > 0;   // otherwise the accumulators were not written
             float part = 0.f;
 #pragma unroll 1
@@ -535,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1) exp_tc_kernel(const __grid_consta
                 uint32_t now[8];
                 __syncwarp();   // the loads below are warp-wide
                 tmem_ld16(acc + c0, r0);
-                if constexpr (GATED) tmem_ld16(acc + 128 + c0, r1);
+                if constexpr (GATED) tmem_ld16(acc + C::NB + c0, r1);
                 if constexpr (C::kTwo) tmem_ld16(accq + c0, r2);
                 if (with_aux) {
 #pragma unroll
@@ -677,14 +690,14 @@ cudaError_t launch_kind(const ExpCall &c, cudaStream_t st) {
         case kDaLin:
             width = s.mlp ? s.h : s.o;
             maps.make(&a.a, c.xrows, s.d, c.point_rows, 0, C::kBoxA);
-            maps.make(&a.b, c.w1, s.d, s.first(), s.K, GATED ? 128 : C::N1 / CG);
+            maps.make(&a.b, c.w1, s.d, s.first(), s.K, GATED ? C::NB : C::N1 / CG);
             break;
         case kDaMlp:
             width = s.h;
             maps.make(&a.a, c.dyrows, s.o, c.point_rows, 0, C::kBoxA);
             maps.make(&a.b, c.w2, s.h, s.o, s.K, kStepK);
             maps.make(&a.a2, c.xrows, s.d, c.point_rows, 0, C::kBoxA);
-            maps.make(&a.b2, c.w1, s.d, s.first(), s.K, GATED ? 128 : C::N2 / CG);
+            maps.make(&a.b2, c.w1, s.d, s.first(), s.K, GATED ? C::NB : C::N2 / CG);
             break;
         case kSecond:
             width = s.o;
@@ -764,6 +777,10 @@ cudaError_t launch_rows_w(const ExpCall &c, cudaStream_t st) {
     return c.rt.tile_rows == 2 * kRowsA ? launch_kind<T, KIND, ACT, GATED, 2, W>(c, st)
                                         : launch_kind<T, KIND, ACT, GATED, 1, W>(c, st);
 }
+// Tiles are 256 weight rows wide, 128 where a result has no more columns.
+// (Choosing 128 or 64 so that short segments fill the last round of SMs more
+// evenly changed nothing: 333 points, 32 experts of 1000-616-520 gated 49 and
+// 51 us, 128 points, 8 experts of 2048-1024-2048 gated 52 and 50.)
 template <typename T, int KIND, int ACT, bool GATED>
 cudaError_t launch_rows(const ExpCall &c, cudaStream_t st) {
     const int width = KIND == kDx ? c.s.d : KIND == kSecond || !c.s.mlp ? c.s.o : 256;
