@@ -85,7 +85,7 @@ Layout layout_of(const ExpShape &p, bool backward, int path) {
         o = align_up(o + bytes);
     };
     const size_t KK = (size_t)p.K + 1;
-    const size_t chunks = p.dense ? 0 : (size_t)((p.P + kExpChunk - 1) / kExpChunk);
+    const size_t chunks = p.dense ? 0 : (size_t)((p.P + exp_chunk(p.K) - 1) / exp_chunk(p.K));
     take(L.cnt, p.dense ? 0 : KK * 4);
     take(L.seg, p.dense ? 0 : (KK + 1) * 4);
     take(L.tile_at, p.dense ? 0 : (size_t)L.max_tiles * 16);
@@ -98,7 +98,7 @@ Layout layout_of(const ExpShape &p, bool backward, int path) {
     const bool sorted = path == 2 && !p.dense;
     take(L.xrows, sorted ? (size_t)L.max_rows * p.d * 2 : 0);
     take(L.dyrows, sorted && backward && p.mlp ? (size_t)L.max_rows * p.o * 2 : 0);
-    const int wide = !backward ? p.o : (p.d > p.o ? p.d : p.o);
+    const int wide = backward ? p.d : p.o;
     take(L.slots, p.direct() ? 0 : (size_t)p.P * wide * 4);
     take(L.rpart, backward ? (size_t)p.P * L.nrpart * 4 : 0);
     // partial bias gradients
@@ -122,6 +122,7 @@ ExpCall make_call(const ExpShape &p, const Layout &L, void *ws, const int32_t *i
     c.rt.ntiles = (int *)(b + L.ntiles);
     c.rt.row_pair = (int *)(b + L.row_pair);
     c.rt.hist = (int *)(b + L.hist);
+    c.rt.chunk = exp_chunk(p.K);
     c.rt.ids = ids;
     c.rt.N = p.N;
     c.rt.P = p.P;
@@ -137,7 +138,7 @@ ExpCall make_call(const ExpShape &p, const Layout &L, void *ws, const int32_t *i
     c.slots = (float *)(b + L.slots);
     c.rpart = (float *)(b + L.rpart);
     c.colpart = (float *)(b + L.colpart);
-    c.max_rows = L.max_rows;
+    c.max_rows = c.da_rows = L.max_rows;
     c.nrpart = L.nrpart;
     c.esize = L.esize;
     return c;
@@ -233,9 +234,15 @@ gmm_status run(ExpCall &c, const ExpShape &p, const Layout &L, int path, bool ba
     if (path == 0) {
         if (e == cudaSuccess) e = launch_exp_simt(c, backward, s);
     } else {
+        const bool plain = backward && c.plain_da();
+        if (plain && !c.s.dense) c.dyrows = c.da;
         if (c.s.dense) {
             c.xrows = const_cast<void *>(c.x);
             c.dyrows = const_cast<void *>(c.dy);
+            if (plain) {
+                c.da = c.dyrows;
+                c.da_rows = p.N;
+            }
         } else if (e == cudaSuccess) {
             e = launch_exp_gather(c, backward, s);
         }

@@ -11,8 +11,9 @@ namespace gmmb {
 // Rows of one expert's segment start at a multiple of kExpTile, so that a
 // tile of rows belongs to one expert.
 constexpr int kExpTile = 128;
-// Pairs per histogram of the routing's sort.
-constexpr int kExpChunk = 64;
+// Pairs per histogram of the routing's sort: short runs for latency, longer
+// ones with many experts, so that the histograms stay within four words a pair.
+inline int exp_chunk(int K) { return K < 256 ? 64 : K < 1024 ? 256 : 1024; }
 
 struct ExpShape {
     int64_t N, P;   // points; (point, entry) pairs, N * max(r, 1)
@@ -41,6 +42,7 @@ struct ExpRoute {
     int *ntiles;        // [2] 128-row and 256-row tiles
     int *row_pair;      // [max rows] pair of each valid row
     int *hist;          // [chunks x (K + 1)]
+    int chunk;          // pairs per chunk, a multiple of 64
     const int32_t *ids; // NULL: dense
     int64_t N, P;
     int K, r;
@@ -88,6 +90,12 @@ struct ExpCall {
     // cores; the arrays themselves in the dense form), and how many
     void *xrows, *dyrows;
     int64_t point_rows;
+    int64_t da_rows;    // rows of da's array
+    // linear form without activation and weights: the pre-activations'
+    // gradient is dY itself, and nothing has to be computed again
+    __host__ __device__ bool plain_da() const {
+        return !s.mlp && s.act == GMM_ACT_NONE && !resp;
+    }
     float *slots, *rpart, *colpart;
     int64_t max_rows;
     int nrpart;         // partial sums of dresp per pair

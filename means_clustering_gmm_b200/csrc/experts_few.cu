@@ -301,6 +301,10 @@ __global__ void __launch_bounds__(kThreads, 4) few_first_kernel(ExpCall c) {
     const T *w0 = base + (size_t)r0 * s.d, *w1 = base + (size_t)r1 * s.d;
     const int chunks = (s.d + 31) / 32;
     const int k0 = chunks * ks / KS * 32, k1 = min(chunks * (ks + 1) / KS * 32, s.d);
+    // (the biases of the row this thread finishes, on their way meanwhile)
+    const int own = min(n0 + (int)threadIdx.x % rows, width - 1);
+    const float bias = b ? value_at(b + own) : 0.f;
+    const float bias_up = GATED && b ? value_at(b + width + own) : 0.f;
     for (int col0 = 0; col0 < total; col0 += kCols) {
         const int cols = min(total - col0, kCols);
         float acc[4][4];
@@ -334,8 +338,8 @@ __global__ void __launch_bounds__(kThreads, 4) few_first_kernel(ExpCall c) {
                 v += part[k][row][col];
                 if (GATED) u += part[k][16 + row][col];
             }
-            float f = act_fast<ACT>(v + (b ? value_at(b + out) : 0.f));
-            if (GATED) f *= u + (b ? value_at(b + width + out) : 0.f);
+            float f = act_fast<ACT>(v + bias);   // (row is the same for every i)
+            if (GATED) f *= u + bias_up;
             const int64_t p = list[col0 + col];
             if (s.mlp) {
                 // rounded to the type: the second product's operand

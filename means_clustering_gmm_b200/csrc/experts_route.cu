@@ -1,8 +1,8 @@
 // Routing of the experts' products and the sums around them.
 //
 // Routing is a stable counting sort of the (point, entry) pairs by expert,
-// as the k-means update sorts points by cluster: histograms of chunks of 64
-// pairs (one warp each), a scan over the chunks per expert, a scan over the
+// as the k-means update sorts points by cluster: histograms of chunks of 64 to
+// 1024 pairs (one warp each), a scan over the chunks per expert, a scan over the
 // experts with every segment rounded up to whole 128-row tiles, a stable
 // scatter.  No floating-point atomics and no order that depends on
 // scheduling, so every later sum over a segment is reproducible.
@@ -10,7 +10,7 @@
 
 namespace gmmb {
 
-constexpr int kChunkPairs = kExpChunk;   // pairs per warp of the sort
+constexpr int kKeys = 2;   // pairs a lane loads at once
 
 // Key of a pair: its expert, or K where it has none.
 __device__ __forceinline__ int pair_key(const int32_t *ids, int64_t p, int K, int *err) {
@@ -26,35 +26,37 @@ exp_hist_kernel(ExpRoute rt, int *err) {
     const int KK = rt.K + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int *row = sh + warp * KK;
     const int64_t chunk = (int64_t)blockIdx.x * 4 + warp;
-    const int64_t p0 = chunk * kChunkPairs;
-    if (p0 >= rt.P) return;
-    int key[kChunkPairs / 32];
-#pragma unroll
-    for (int u = 0; u < kChunkPairs / 32; ++u) {
-        const int64_t p = p0 + u * 32 + lane;
-        key[u] = p < rt.P ? pair_key(rt.ids, p, rt.K, err) : -1;
-    }
+    const int64_t beg = chunk * rt.chunk, end = min(beg + rt.chunk, rt.P);
+    if (beg >= rt.P) return;
     for (int e = lane; e < KK; e += 32) row[e] = 0;
     __syncwarp();
+    for (int64_t p0 = beg; p0 < end; p0 += 32 * kKeys) {
+        int key[kKeys];
 #pragma unroll
-    for (int u = 0; u < kChunkPairs / 32; ++u) {
-        const unsigned same = __match_any_sync(0xffffffffu, key[u]);
-        if (key[u] >= 0 && lane == __ffs(same) - 1) row[key[u]] += __popc(same);
-        __syncwarp();
+        for (int u = 0; u < kKeys; ++u) {
+            const int64_t p = p0 + u * 32 + lane;
+            key[u] = p < end ? pair_key(rt.ids, p, rt.K, err) : -1;
+        }
+#pragma unroll
+        for (int u = 0; u < kKeys; ++u) {
+            const unsigned same = __match_any_sync(0xffffffffu, key[u]);
+            if (key[u] >= 0 && lane == __ffs(same) - 1) row[key[u]] += __popc(same);
+            __syncwarp();
+        }
     }
     for (int e = lane; e < KK; e += 32) rt.hist[chunk * KK + e] = row[e];
 }
 
-// One warp per key: exclusive scan of its counts over the chunks, in place.
-__global__ void __launch_bounds__(128)
+// One block per key: exclusive scan of its counts over the chunks, in place.
+__global__ void __launch_bounds__(1024)
 exp_scan_kernel(ExpRoute rt, int64_t nch) {
     exp_enter();
-    const int KK = rt.K + 1, lane = threadIdx.x & 31;
-    const int e = blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (e >= KK) return;
+    __shared__ int wsum[32];
+    const int KK = rt.K + 1, e = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int warps = blockDim.x >> 5;
     int total = 0;
-    for (int64_t c0 = 0; c0 < nch; c0 += 32) {
-        const int64_t c = c0 + lane;
+    for (int64_t c0 = 0; c0 < nch; c0 += blockDim.x) {
+        const int64_t c = c0 + threadIdx.x;
         const int v = c < nch ? rt.hist[c * KK + e] : 0;
         int x = v;
 #pragma unroll
@@ -62,12 +64,20 @@ exp_scan_kernel(ExpRoute rt, int64_t nch) {
             const int y = __shfl_up_sync(0xffffffffu, x, o);
             if (lane >= o) x += y;
         }
+        if (lane == 31) wsum[warp] = x;
+        __syncthreads();
+        int all = 0;
+        for (int w = 0; w < warps; ++w) {
+            if (w < warp) x += wsum[w];
+            all += wsum[w];
+        }
         if (c < nch) rt.hist[c * KK + e] = total + x - v;
-        total += __shfl_sync(0xffffffffu, x, 31);
+        total += all;
+        __syncthreads();
     }
     // points without an expert make rows only where the last product writes
     // the result itself
-    if (lane == 0) rt.cnt[e] = e < rt.K || rt.r <= 1 ? total : 0;
+    if (threadIdx.x == 0) rt.cnt[e] = e < rt.K || rt.r <= 1 ? total : 0;
 }
 
 // One block of 1024: segment starts (whole tiles) and the tables of 128-row
@@ -231,28 +241,30 @@ exp_scatter_kernel(ExpRoute rt) {
     const int KK = rt.K + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int *row = sh + warp * KK;   // next row of each expert for this chunk
     const int64_t chunk = (int64_t)blockIdx.x * 4 + warp;
-    const int64_t p0 = chunk * kChunkPairs;
-    if (p0 >= rt.P) return;
-    int key[kChunkPairs / 32];
-#pragma unroll
-    for (int u = 0; u < kChunkPairs / 32; ++u) {
-        const int64_t p = p0 + u * 32 + lane;
-        key[u] = p < rt.P ? pair_key(rt.ids, p, rt.K, nullptr) : -1;
-        if (key[u] == rt.K && rt.r > 1) key[u] = -1;
-    }
+    const int64_t beg = chunk * rt.chunk, end = min(beg + rt.chunk, rt.P);
+    if (beg >= rt.P) return;
     for (int e = lane; e < KK; e += 32) row[e] = rt.seg[e] + rt.hist[chunk * KK + e];
     __syncwarp();
+    for (int64_t p0 = beg; p0 < end; p0 += 32 * kKeys) {
+        int key[kKeys];
 #pragma unroll
-    for (int u = 0; u < kChunkPairs / 32; ++u) {
-        const unsigned same = __match_any_sync(0xffffffffu, key[u]);
-        const int rank = __popc(same & ((1u << lane) - 1));
-        const int base = key[u] >= 0 ? row[key[u]] : 0;
-        __syncwarp();
-        if (key[u] >= 0) {
-            rt.row_pair[base + rank] = (int)(p0 + u * 32 + lane);
-            if (rank == 0) row[key[u]] = base + __popc(same);
+        for (int u = 0; u < kKeys; ++u) {
+            const int64_t p = p0 + u * 32 + lane;
+            key[u] = p < end ? pair_key(rt.ids, p, rt.K, nullptr) : -1;
+            if (key[u] == rt.K && rt.r > 1) key[u] = -1;
         }
-        __syncwarp();
+#pragma unroll
+        for (int u = 0; u < kKeys; ++u) {
+            const unsigned same = __match_any_sync(0xffffffffu, key[u]);
+            const int rank = __popc(same & ((1u << lane) - 1));
+            const int base = key[u] >= 0 ? row[key[u]] : 0;
+            __syncwarp();
+            if (key[u] >= 0) {
+                rt.row_pair[base + rank] = (int)(p0 + u * 32 + lane);
+                if (rank == 0) row[key[u]] = base + __popc(same);
+            }
+            __syncwarp();
+        }
     }
 }
 
@@ -269,7 +281,7 @@ cudaError_t launch_exp_route(const ExpCall &c, cudaStream_t s) {
         if (e != cudaSuccess) return e;
         return exp_launch(exp_route_kernel, dim3(1), 1024, bytes, s, rt, c.err);
     }
-    const int64_t nch = (rt.P + kChunkPairs - 1) / kChunkPairs;
+    const int64_t nch = (rt.P + rt.chunk - 1) / rt.chunk;
     const unsigned blocks = (unsigned)((nch + 3) / 4);
     const int smem = 4 * KK * (int)sizeof(int);
     cudaError_t e;
@@ -281,7 +293,8 @@ cudaError_t launch_exp_route(const ExpCall &c, cudaStream_t s) {
         if (e != cudaSuccess) return e;
     }
     e = exp_launch(exp_hist_kernel, dim3(blocks), 128, smem, s, rt, c.err);
-    if (e == cudaSuccess) e = exp_launch(exp_scan_kernel, dim3((KK + 3) / 4), 128, 0, s, rt, nch);
+    if (e == cudaSuccess)
+        e = exp_launch(exp_scan_kernel, dim3(KK), nch > 256 ? 1024 : 256, 0, s, rt, nch);
     if (e == cudaSuccess)
         e = exp_launch(exp_tiles_kernel, dim3(1), 1024, 2 * (KK + 1) * sizeof(int), s, rt);
     if (e == cudaSuccess) e = exp_launch(exp_scatter_kernel, dim3(blocks), 128, smem, s, rt);
@@ -322,8 +335,10 @@ exp_gather_kernel(ExpRoute rt, const uint4 *__restrict__ x, uint4 *__restrict__ 
 
 cudaError_t launch_exp_gather(const ExpCall &c, bool backward, cudaStream_t s) {
     const int64_t want = (c.max_rows + 31) / 32;
-    // (the linear form's gradients read dY through the pairs instead)
-    const dim3 grid((unsigned)(want < 148 * 8 ? want : 148 * 8), backward && c.s.mlp ? 2 : 1);
+    // (the linear form's gradients read dY through the pairs instead, or take
+    // its rows as they are)
+    const bool dy = backward && (c.s.mlp || c.plain_da());
+    const dim3 grid((unsigned)(want < 148 * 8 ? want : 148 * 8), dy ? 2 : 1);
     return exp_launch(exp_gather_kernel, grid, 256, 0, s, c.rt, (const uint4 *)c.x,
                       (uint4 *)c.xrows, c.s.d / 8, (const uint4 *)c.dy, (uint4 *)c.dyrows,
                       c.s.o / 8);

@@ -706,13 +706,13 @@ cudaError_t launch_kind(const ExpCall &c, cudaStream_t st) {
             break;
         case kDx:
             width = s.d;
-            maps.make(&a.a, c.da, s.first(), c.max_rows, 0, C::kBoxA);
+            maps.make(&a.a, c.da, s.first(), c.da_rows, 0, C::kBoxA);
             maps.make(&a.b, c.w1, s.d, s.first(), s.K, kStepK);
             break;
         case kDw1:
             width = s.d;
             mrows = s.first();
-            maps.make(&a.a, c.da, s.first(), c.max_rows, 0, kStepK);
+            maps.make(&a.a, c.da, s.first(), c.da_rows, 0, kStepK);
             maps.make(&a.b, c.xrows, s.d, c.point_rows, 0, kStepK);
             break;
         case kDw2:
@@ -809,7 +809,7 @@ cudaError_t run_tc(const ExpCall &c, bool backward, cudaStream_t st) {
         return e;
     }
     if (c.s.mlp) e = launch_rows<T, kDaMlp, ACT, GATED>(c, st);
-    else e = launch_rows<T, kDaLin, ACT, false>(c, st);
+    else e = c.plain_da() ? cudaSuccess : launch_rows<T, kDaLin, ACT, false>(c, st);
     if (e == cudaSuccess) e = launch_rows<T, kDx, GMM_ACT_NONE, false>(c, st);
     if (e == cudaSuccess) e = launch_grad<T, kDw1>(c, st);
     if (e == cudaSuccess && c.s.mlp) e = launch_grad<T, kDw2>(c, st);

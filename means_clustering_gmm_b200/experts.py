@@ -13,7 +13,8 @@ components and add the results up by responsibility.  k-means ids serve as
 
 Argument marshalling only, as in ``api``; include/gmm_b200.h states each
 operation.  Calls that share a workspace must not overlap in time on the
-device (two captured graphs that may run at once need one each).
+device (two captured graphs that may run at once need one each).  An id at or
+above K is skipped and recorded: ``gmm_last_error(ws)`` reports GMM_ERR_RANGE.
 """
 from __future__ import annotations
 
@@ -51,7 +52,7 @@ def _shape(N, d, h, o, K, r, dtype, activation="none", gated=False):
     return p
 
 
-def expert_workspace_size(N: int, d: int, h: int, o: int, K: int, r: int, dtype=torch.bfloat16,
+def expert_workspace_size(N: int, d: int, h: int, o: int, K: int, r: int, dtype=torch.float32,
                           gated: bool = False, backward: bool = False,
                           flags: int = GMM_FLAG_NONE) -> int:
     """Bytes of workspace of expert_linear (h = 0) or expert_mlp, 0 for invalid
@@ -60,7 +61,7 @@ def expert_workspace_size(N: int, d: int, h: int, o: int, K: int, r: int, dtype=
         _shape(N, d, h, o, K, r, dtype, gated=gated), int(backward), int(flags)))
 
 
-def expert_path(N: int, d: int, h: int, o: int, K: int, r: int, dtype=torch.bfloat16,
+def expert_path(N: int, d: int, h: int, o: int, K: int, r: int, dtype=torch.float32,
                 gated: bool = False, backward: bool = False, flags: int = GMM_FLAG_NONE) -> int:
     """Which kernels a call of these sizes runs: 0 CUDA cores, 1 the form for
     few points, 2 tensor cores (gmm_expert_path)."""

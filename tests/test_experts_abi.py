@@ -120,11 +120,12 @@ def test_binding_refuses_on_the_host():
         gmm.Workspace.for_expert_linear(0, 8, 8, 1, 0, torch.float32)
     with pytest.raises(ValueError):
         gmm.expert_path(1, 8, 0, 8, 2, 0)
-    assert gmm.expert_path(64, 8, 0, 8, 9, 4) == 1
-    assert gmm.expert_path(64, 8, 16, 8, 9, 5) == 2       # more pairs
-    assert gmm.expert_path(65, 8, 16, 8, 9, 1) == 2       # more points
-    assert gmm.expert_path(1, 8, 16, 8, 9, 1, backward=True) == 2
-    assert gmm.expert_path(100, 7, 0, 8, 2, 1) == 2       # on padded copies
-    assert gmm.expert_path(5, 7, 0, 8, 2, 1) == 2
+    bf = torch.bfloat16
+    assert gmm.expert_path(64, 8, 0, 8, 9, 4, bf) == 1
+    assert gmm.expert_path(64, 8, 16, 8, 9, 5, bf) == 2       # more pairs
+    assert gmm.expert_path(65, 8, 16, 8, 9, 1, bf) == 2       # more points
+    assert gmm.expert_path(1, 8, 16, 8, 9, 1, bf, backward=True) == 2
+    assert gmm.expert_path(100, 7, 0, 8, 2, 1, bf) == 2       # on padded copies
+    assert gmm.expert_path(5, 7, 0, 8, 2, 1, bf) == 2
     assert gmm.expert_path(100, 8, 0, 8, 2, 1, torch.float32) == 0
-    assert gmm.expert_path(100, 8, 0, 8, 2, 1, flags=gmm.GMM_FLAG_FORCE_SIMT) == 0
+    assert gmm.expert_path(100, 8, 0, 8, 2, 1, bf, flags=gmm.GMM_FLAG_FORCE_SIMT) == 0

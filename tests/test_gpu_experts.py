@@ -249,6 +249,11 @@ LINEAR = [
     (385, 64, 64, 1, 0, "bf16", "gelu", {"res": True}),
     (5000, 16, 8, 3, 8, "bf16", "none", {"cut": 0.5}),                    # 40000 pairs
     (600, 16, 8, 2000, 2, "f16", "none", {"cut": 0.1}),                   # many experts
+    (9000, 16, 8, 400, 1, "bf16", "silu", {"cut": 0.1}),
+    (9000, 8, 8, 1, 4, "bf16", "silu", {"cut": 0.1}),                     # one, many times
+    (700, 72, 136, 3, 2, "bf16", "none", {"cut": 0.2, "resp": False}),    # dz is dY itself
+    (300, 72, 136, 1, 0, "f16", "none", {}),
+    (300, 71, 135, 1, 0, "f16", "none", {}),
     (64, 136, 72, 1, 0, "bf16", "gelu", {"res": True}),
     (2, 1032, 4000, 1, 0, "f16", "silu", {"res": True}),
     (64, 200, 40, 3, 4, "bf16", "silu", {"cut": 0.3, "res": True}),
@@ -364,7 +369,9 @@ def test_nan_stays_with_its_point(flags, N):
     clean_g = backward(cuda(s), "silu", flags=flags)[0]
     assert clean.isfinite().all() and all(t.isfinite().all() for t in clean_g.values())
     s["ids"][3] = -1
-    s["x"][3] = float("nan")
+    s["resp"][3] = float("nan")
+    for k in ("x", "dy"):
+        s[k][3] = float("nan")
     s["x"][7] = float("nan")
     s["ids"][7] = torch.tensor([2, -1])
     y = forward(cuda(s), "silu", flags=flags)[0]
@@ -375,6 +382,96 @@ def test_nan_stays_with_its_point(flags, N):
     for k in ("dw1", "dw2", "db1", "db2"):
         assert g[k][[0, 1, 3, 4, 5]].isfinite().all(), k
     assert g["dw1"][2].isnan().any()
+
+
+@pytest.mark.parametrize("N", [3, 40, 700])
+@pytest.mark.parametrize("h", [0, 72])
+def test_element_aligned_biases_and_residual(N, h):
+    """Biases and the residual may start at any element; everything else at
+    any 16 bytes (not more)."""
+    s = inputs(31, N, 64, h, 72, 2, 2 if h else 1, "bf16", res=True)
+    want = forward(cuda(s), "gelu")[0], backward(cuda(s), "gelu")[0]
+    c = {}
+    for k, t in s.items():
+        off = {"b1": 1, "b2": 3, "res": 5}.get(k, 8)
+        if t is None or k in ("ids", "resp"):
+            c[k] = None if t is None else t.cuda()
+            continue
+        room = torch.empty(t.numel() + off, dtype=t.dtype, device="cuda")
+        c[k] = room[off:].view(t.shape).copy_(t)
+    assert torch.equal(forward(c, "gelu")[0], want[0])
+    got = backward(c, "gelu")[0]
+    assert all(torch.equal(got[k], want[1][k]) for k in got)
+    out = torch.empty(N * 72 + 8, dtype=torch.bfloat16, device="cuda")[8:].view(N, 72)
+    assert torch.equal(forward(c, "gelu", out=out)[0], want[0])
+
+
+@pytest.mark.parametrize("K,r,N", [(40, 2, 1), (40, 2, 300)])
+def test_weights_past_32_bits(K, r, N):
+    """The last expert's weights lie past 2^32 elements."""
+    d, o = 4096, 32768
+    s = inputs(32, N, d, 0, 8, 1, r, "bf16", bias=False)
+    w = torch.zeros(K, o, d, dtype=torch.bfloat16, device="cuda")
+    cols = 264
+    rows = (torch.randn(cols, d, generator=torch.Generator().manual_seed(3)) / 64).bfloat16()
+    w[K - 1, o - cols:] = rows.cuda()
+    assert w.numel() > 2 ** 32
+    s["ids"] = torch.full((N, r), K - 1, dtype=torch.int32)
+    s["ids"][:, 1] = -1
+    c = cuda(s)
+    ws = gmm.Workspace.for_expert_linear(N, d, o, K, r, torch.bfloat16)
+    y = gmm.expert_linear(c["x"], c["ids"], c["resp"], w, None, ws)
+    assert gmm.gmm_last_error(ws) == 0
+    assert not y[:, :o - cols].any()
+    x = s["x"].double()
+    g = s["resp"][:, :1].double()
+    v = g * (x @ rows.double().T)
+    b = gamma(d) * g * (x.abs() @ rows.double().abs().T)
+    b += half_step(torch.bfloat16) * (v.abs() + b)
+    assert ((y[:, o - cols:].cpu().double() - v).abs() <= b).all()
+
+
+def test_points_past_32_bits():
+    """Rows of X and Y past 2^32 elements, dense and routed."""
+    N, d, o = (1 << 25) + 300, 128, 8
+    x = torch.zeros(N, d, dtype=torch.bfloat16, device="cuda")
+    tail = torch.randn(512, d, generator=torch.Generator().manual_seed(4)).bfloat16()
+    x[N - 512:] = tail.cuda()
+    w = torch.randn(2, o, d, generator=torch.Generator().manual_seed(5)).bfloat16()
+    for r in (0, 1):
+        k = 2 if r else 1
+        ids = None
+        if r:
+            ids = torch.zeros(N, 1, dtype=torch.int32, device="cuda")
+            ids[N - 512::2] = 1
+        ws = gmm.Workspace.for_expert_linear(N, d, o, k, r, torch.bfloat16)
+        y = gmm.expert_linear(x, ids, None, w[:k].contiguous().cuda(), None, ws)
+        assert gmm.gmm_last_error(ws) == 0 and not y[:N - 512].any()
+        e = torch.zeros(512, dtype=torch.long)
+        if r:
+            e[::2] = 1
+        t = tail.double()
+        v = torch.einsum("nd,nod->no", t, w.double()[e])
+        b = gamma(d) * torch.einsum("nd,nod->no", t.abs(), w.double()[e].abs())
+        b += half_step(torch.bfloat16) * (v.abs() + b)
+        assert ((y[N - 512:].cpu().double() - v).abs() <= b).all()
+        del ws, y
+
+
+def test_capture_of_a_first_call():
+    """Sizes whose kernels may not have run yet, captured at once."""
+    c = cuda(inputs(33, 70, 72, 88, 40, 3, 2, "f16", gated=True, bias=False))
+    ws = workspace(c, True, True)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y, _ = forward(c, "none", True, ws=ws)
+        g, _ = backward(c, "none", True, ws=ws)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, forward(c, "none", True)[0])
+    want = backward(c, "none", True)[0]
+    assert all(torch.equal(g[k], want[k]) for k in want)
 
 
 @pytest.mark.parametrize("N", [1, 50, 200])
