@@ -539,10 +539,22 @@ __global__ void __launch_bounds__(kThreads, 1) exp_tc_kernel(const __grid_consta
                                                               next_col));
             const bool has = j.steps1 > 0;   // otherwise the accumulators were not written
             float part = 0.f;
+            // the accumulators go back as soon as they are in registers
+            auto release = [&] {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (CG == 2)
+                        mbar_arrive_cluster_cta(mapa_u32(&bars->accfree[buf], 0));
+                    else
+                        mbar_arrive(&bars->accfree[buf]);
+                }
+            };
+            const int columns = min(width - cw, kPart);   // of this warp
+            if (columns <= 0) release();
 #pragma unroll 1
-            for (int c0 = pt * kPart; c0 < (pt + 1) * kPart; c0 += 16) {
-                const int col = j.col0 + c0;
-                if (col >= width) break;
+            for (int at = 0; at < columns; at += 16) {
+                const int c0 = pt * kPart + at, col = j.col0 + c0;
                 const bool both = col + 8 < width;
                 uint32_t r0[16], r1[16], r2[16];
                 uint32_t now[8];
@@ -556,6 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1) exp_tc_kernel(const __grid_consta
                     if (c0 + 16 < (pt + 1) * kPart) fetch(col + 16);
                 }
                 tmem_ld_wait();
+                if (at + 16 >= columns) release();
                 float2 x[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) x[i] = pair_of(r0, i);
@@ -657,12 +670,6 @@ __global__ void __launch_bounds__(kThreads, 1) exp_tc_kernel(const __grid_consta
             if constexpr (KIND == kDaLin || KIND == kDaMlp) {
                 if (valid && !none && c.dresp && cw < width)
                     c.rpart[pair * c.nrpart + cw / kPart] = part;
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                if constexpr (CG == 2) mbar_arrive_cluster(mapa_u32(&bars->accfree[buf], 0));
-                else mbar_arrive(&bars->accfree[buf]);
             }
         }
     }

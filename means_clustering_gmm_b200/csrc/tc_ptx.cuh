@@ -333,6 +333,14 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t caddr) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(caddr)
                  : "memory");
 }
+// The same without waiting for this thread's earlier writes outside the CTA
+// (release at CTA scope): for a barrier that hands back TMEM columns, whose
+// reads are complete, where a cluster-scope release would wait until the
+// tile's global stores have landed.
+__device__ __forceinline__ void mbar_arrive_cluster_cta(uint32_t caddr) {
+    asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(caddr)
+                 : "memory");
+}
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t *bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
