@@ -119,10 +119,8 @@ struct Lists {
     int segs;
 };
 
-// Threads 0..255, one per pair; the others only take part in the barriers.
-// ONCE: a pair that repeats its point's expert has no entry of its own; its
-// weight goes to the first one's.
-template <bool ONCE>
+// One thread per pair.  A pair that repeats its point's expert has no entry of
+// its own; its weight goes to the first one's.
 __device__ __forceinline__ void make_lists(const ExpCall &c, Lists &L) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int P = (int)c.s.P, r = c.rt.r;
@@ -142,12 +140,12 @@ __device__ __forceinline__ void make_lists(const ExpCall &c, Lists &L) {
             const unsigned same = __match_any_sync(0xffffffffu, id);
             // this pair's point's entries, before it and from it on
             const int p0 = lane / r * r;
-            const unsigned point = (r < 32 ? (1u << r) - 1 : 0xffffffffu) << p0;
-            const bool repeat = ONCE && (same & point & ((1u << lane) - 1));
+            const unsigned point = ((1u << r) - 1) << p0;
+            const bool repeat = (same & point & ((1u << lane) - 1)) != 0;
             float weight = own;
             for (int i = 1; i < r; ++i) {
                 const float w = __shfl_down_sync(0xffffffffu, own, i);
-                if (ONCE && lane + i < p0 + r && (same >> (lane + i) & 1)) weight += w;
+                if (lane + i < p0 + r && lane + i < 32 && (same >> (lane + i) & 1)) weight += w;
             }
             const unsigned entries = __ballot_sync(0xffffffffu, id >= 0 && !repeat);
             const unsigned mine = same & entries;
@@ -174,22 +172,20 @@ __device__ __forceinline__ void make_lists(const ExpCall &c, Lists &L) {
         __syncthreads();
         return;
     }
-    if (tid < kPairs) {
-        L.ids[tid] = id;
-        L.weight[tid] = own;
-    }
+    L.ids[tid] = id;
+    L.weight[tid] = own;
     __syncthreads();
     float weight = 0.f;
     if (id >= 0) {
         const int p0 = tid / r * r;
         for (int q = p0; q < p0 + r; ++q) {
             const bool same = L.ids[q] == id;
-            if (ONCE && same && q < tid) id = -1;
-            if (same && (ONCE ? q >= tid : q == tid)) weight += L.weight[q];
+            if (same && q < tid) id = -1;
+            if (same && q >= tid) weight += L.weight[q];
         }
     }
     __syncthreads();
-    if (tid < kPairs) L.ids[tid] = id;
+    L.ids[tid] = id;
     __syncthreads();
     int first = kPairs, rank = 0, count = 0;
     if (id >= 0) {
@@ -219,7 +215,7 @@ __device__ __forceinline__ void make_lists(const ExpCall &c, Lists &L) {
         const int y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
     }
-    if (warp < kWarps && lane == 31) L.wsum[warp] = x;
+    if (lane == 31) L.wsum[warp] = x;
     __syncthreads();
     int before = x - v, total = 0;
     for (int w = 0; w < kWarps; ++w) {
@@ -367,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 3) few_second_kernel(ExpCall c, int 
     float *mine = sums + warp * N * 16, *block = sums + kWarps * N * 16;
     for (int i = tid; i < kWarps * N * 16; i += kThreads) sums[i] = 0.f;
     // ids and weights do not depend on the first kernel
-    make_lists<true>(c, L);
+    make_lists(c, L);
     // this warp's part of the segments' 32-index chunks, laid end to end
     const int per = (s.h + 31) / 32, total = L.segs * per;
     const int w = rank * kWarps + warp, warps = C * kWarps;

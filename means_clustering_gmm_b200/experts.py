@@ -13,7 +13,10 @@ components and add the results up by responsibility.  k-means ids serve as
 
 Argument marshalling only, as in ``api``; include/gmm_b200.h states each
 operation.  Calls that share a workspace must not overlap in time on the
-device (two captured graphs that may run at once need one each).  An id at or
+device (two captured graphs that may run at once need one each).  ``stream``
+(default: the current one of X's device) is where a call runs and its outputs
+belong; its inputs have to be ready there.  Bases of X, dY, the weights and
+``out`` must be 16-byte aligned (whole tensors are).  An id at or
 above K is skipped and recorded: ``gmm_last_error(ws)`` reports GMM_ERR_RANGE.
 """
 from __future__ import annotations
