@@ -102,9 +102,8 @@ Layout layout_of(const ExpShape &p, bool backward, int path) {
     take(L.slots, p.direct() ? 0 : (size_t)p.P * wide * 4);
     take(L.rpart, backward ? (size_t)p.P * L.nrpart * 4 : 0);
     // partial bias gradients
-    const size_t cols = backward && path == 2
-                            ? (size_t)exp_colsum_slices(p) * (p.first() + (p.mlp ? p.o : 0))
-                            : 0;
+    const size_t cols =
+        backward ? (size_t)exp_colsum_slices(p) * (p.first() + (p.mlp ? p.o : 0)) : 0;
     take(L.colpart, cols * p.K * 4);
     L.total = o;
     return L;

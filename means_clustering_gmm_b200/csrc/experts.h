@@ -66,7 +66,10 @@ struct ExpRoute {
     __device__ __forceinline__ int64_t pair(int64_t row) const {
         return ids ? row_pair[row] : row;
     }
-    __device__ __forceinline__ int64_t token(int64_t p) const { return r > 1 ? p / r : p; }
+    // pairs of more than one entry a point fit 31 bits
+    __device__ __forceinline__ int64_t token(int64_t p) const {
+        return r > 1 ? (uint32_t)p / (uint32_t)r : p;
+    }
     __device__ __forceinline__ bool used(int64_t p) const {
         return !ids || (ids[p] >= 0 && ids[p] < K);
     }

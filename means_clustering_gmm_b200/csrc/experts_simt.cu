@@ -1,33 +1,39 @@
 // The experts' products on CUDA cores, for fp32 and for widths or pointers
-// the tensor-core kernels do not take.  Every product is a 64 x 64 tile with
-// a 4 x 4 micro tile per thread, fp32 throughout; what one product hands to
-// the next stays fp32 in the workspace.
+// the tensor-core kernels do not take.  Every product is a tile of 16 R x 64
+// with an R x 4 micro tile per thread, fp32 throughout; what one product hands
+// to the next stays fp32 in the workspace.  Bound by the FMA pipes and what
+// feeds them from shared memory: 35 TFLOP/s at 4096 x 512 x 512 (R = 8; 30 with
+// R = 4, 23 with R = 2), 25 in a backward pass of 8192 pairs of 512-512-512.
+#include <type_traits>
+
 #include "experts.h"
 
 namespace gmmb {
 
-constexpr int kB = 64, kBK = 32;
+constexpr int kB = 64, kBK = 32, kSms = 148;
 
 // Column m of contraction index k sits at m ^ 4 (k / 4 % 8): four indices of a
 // row stored one by one meet 32 banks, and four columns stay together.
 __device__ __forceinline__ int at_col(int k, int m) { return m ^ ((k >> 2 & 7) << 2); }
 
-struct SimtSmem {
-    float a[2][kBK][kB], b[2][kBK][kB];
+// A tile has 16 R rows, R per thread, and kB columns, four per thread.
+template <int R> struct SimtSmem {
+    float a[2][kBK][16 * R], b[2][kBK][kB];
 };
 
 // Operands.  KROW: row(m) is the array's row of tile row m (NULL outside),
 // contiguous along the contraction; otherwise row(k) is the row of
 // contraction index k, contiguous along the tile's rows, of which `cols` from
 // column c0 exist.
-template <typename E_> struct GatherRows {   // row tok[m] of [. x ld]
+template <typename E_> struct GatherRows {   // the segment's m-th point of [. x ld]
     using E = E_;
     static constexpr bool KROW = true;
     const E *p;
-    const int64_t *tok;
+    ExpRoute rt;
+    int64_t row0;
     int valid, ld;
     __device__ __forceinline__ const E *row(int m) const {
-        return m < valid ? p + tok[m] * ld : nullptr;
+        return m < valid ? p + rt.token(rt.pair(row0 + m)) * ld : nullptr;
     }
 };
 template <typename E_> struct PlainRows {    // rows m0 + m of [rows x ld]
@@ -60,30 +66,32 @@ template <typename E_> struct PointCols {    // columns of the segment's k-th po
     }
 };
 
-// A thread's eight elements of a 64 x 32 operand tile, between global and
-// shared memory.  VEC (fp32, rows of whole 16-byte units): two float4.
-template <class OP, bool VEC> struct Part {
-    float r[8];
-    const typename OP::E *p[OP::KROW ? (VEC ? 2 : 8) : 1];
+// A thread's W / 8 elements of a W x 32 operand tile, between global and
+// shared memory.  VEC (fp32, rows of whole 16-byte units): in float4.
+template <class OP, int W, bool VEC> struct Part {
+    static constexpr int kN = W / (VEC ? 32 : 8);    // loads
+    static constexpr int kCols = VEC ? W / 4 : W;    // threads along a row of the tile
+    float r[W / 8];
+    const typename OP::E *p[OP::KROW ? kN : 1];
     __device__ __forceinline__ void begin(const OP &op) {
         const int tid = threadIdx.x;
         if constexpr (OP::KROW)
 #pragma unroll
-            for (int i = 0; i < (VEC ? 2 : 8); ++i)
+            for (int i = 0; i < kN; ++i)
                 p[i] = op.row(VEC ? (tid >> 3) + 32 * i : (tid >> 5) + 8 * i);
     }
     __device__ __forceinline__ void load(const OP &op, int64_t k0, int64_t K) {
         const int tid = threadIdx.x;
 #pragma unroll
-        for (int i = 0; i < (VEC ? 2 : 8); ++i) {
+        for (int i = 0; i < kN; ++i) {
             if constexpr (VEC) {
                 float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
                 if constexpr (OP::KROW) {
                     const int64_t k = k0 + (tid & 7) * 4;
                     if (p[i] && k < K) v = *reinterpret_cast<const float4 *>(p[i] + k);
                 } else {
-                    const int64_t k = k0 + (tid >> 4) + 16 * i;
-                    const int n = (tid & 15) * 4;
+                    const int64_t k = k0 + tid / kCols + 256 / kCols * i;
+                    const int n = tid % kCols * 4;
                     if (k < K && n < op.cols())
                         v = *reinterpret_cast<const float4 *>(op.row(k) + n);
                 }
@@ -95,42 +103,57 @@ template <class OP, bool VEC> struct Part {
                 const int64_t k = k0 + (tid & 31);
                 r[i] = p[i] && k < K ? value_at(p[i] + k) : 0.f;
             } else {
-                const int64_t k = k0 + (tid >> 6) + 4 * i;
-                const int n = tid & 63;
+                const int64_t k = k0 + tid / kCols + 256 / kCols * i;
+                const int n = tid % kCols;
                 r[i] = k < K && n < op.cols() ? value_at(op.row(k) + n) : 0.f;
             }
         }
     }
-    __device__ __forceinline__ void store(float (&sh)[kBK][kB]) const {
+    __device__ __forceinline__ void store(float (&sh)[kBK][W]) const {
         const int tid = threadIdx.x;
 #pragma unroll
-        for (int i = 0; i < (VEC ? 2 : 8); ++i) {
+        for (int i = 0; i < kN; ++i) {
             if constexpr (VEC && OP::KROW) {
                 const int k = (tid & 7) * 4, m = (tid >> 3) + 32 * i;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) sh[k + j][at_col(k, m)] = r[4 * i + j];
             } else if constexpr (VEC) {
-                const int k = (tid >> 4) + 16 * i;
-                *reinterpret_cast<float4 *>(&sh[k][at_col(k, (tid & 15) * 4)]) =
+                const int k = tid / kCols + 256 / kCols * i;
+                *reinterpret_cast<float4 *>(&sh[k][at_col(k, tid % kCols * 4)]) =
                     make_float4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
             } else {
-                const int k = OP::KROW ? tid & 31 : (tid >> 6) + 4 * i;
-                const int m = OP::KROW ? (tid >> 5) + 8 * i : tid & 63;
+                const int k = OP::KROW ? tid & 31 : tid / kCols + 256 / kCols * i;
+                const int m = OP::KROW ? (tid >> 5) + 8 * i : tid % kCols;
                 sh[k][at_col(k, m)] = r[i];
             }
         }
     }
 };
 
-// acc[i][j] += sum_k A(ty * 4 + i, k) B(tx * 4 + j, k).  The next 32 indices
+// A thread's R x 4 sums, two rows to a register pair: the packed fma leaves
+// every other issue slot to the loads from shared memory.
+template <int R> struct Acc {
+    float2 v[R / 2][4];
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < R / 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[i][j] = make_float2(0.f, 0.f);
+    }
+    __device__ __forceinline__ float at(int i, int j) const {
+        return i & 1 ? v[i >> 1][j].y : v[i >> 1][j].x;
+    }
+};
+
+// acc(i, j) += sum_k A(ty * R + i, k) B(tx * 4 + j, k).  The next 32 indices
 // are on their way into registers while these are multiplied, and shared
 // memory is double-buffered: one barrier a step.
-template <bool VEC, class A, class B>
-__device__ __forceinline__ void simt_mma(SimtSmem &sh, float (&acc)[4][4], int64_t K, const A &opa,
+template <bool VEC, int R, class A, class B>
+__device__ __forceinline__ void simt_mma(SimtSmem<R> &sh, Acc<R> &acc, int64_t K, const A &opa,
                                          const B &opb) {
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    Part<A, VEC> pa;
-    Part<B, VEC> pb;
+    Part<A, 16 * R, VEC> pa;
+    Part<B, kB, VEC> pb;
     pa.begin(opa);
     pb.begin(opb);
     pa.load(opa, 0, K);
@@ -147,47 +170,54 @@ __device__ __forceinline__ void simt_mma(SimtSmem &sh, float (&acc)[4][4], int64
         }
 #pragma unroll
         for (int k = 0; k < kBK; ++k) {
-            const float4 av = *reinterpret_cast<const float4 *>(&sh.a[buf][k][at_col(k, ty * 4)]);
+            float2 a[R / 2];
+            if constexpr (R == 2) {
+                a[0] = *reinterpret_cast<const float2 *>(&sh.a[buf][k][at_col(k, ty * 2)]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < R; i += 4) {
+                    const float4 v =
+                        *reinterpret_cast<const float4 *>(&sh.a[buf][k][at_col(k, ty * R + i)]);
+                    a[i / 2] = make_float2(v.x, v.y);
+                    a[i / 2 + 1] = make_float2(v.z, v.w);
+                }
+            }
             const float4 bv = *reinterpret_cast<const float4 *>(&sh.b[buf][k][at_col(k, tx * 4)]);
-            const float a[4] = {av.x, av.y, av.z, av.w}, b[4] = {bv.x, bv.y, bv.z, bv.w};
+            const float b[4] = {bv.x, bv.y, bv.z, bv.w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < R / 2; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
+                for (int j = 0; j < 4; ++j)
+                    acc.v[i][j] = __ffma2_rn(a[i], make_float2(b[j], b[j]), acc.v[i][j]);
         }
     }
 }
 
-__device__ __forceinline__ void zero(float (&acc)[4][4]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
-}
-
-// A block's 64 rows: half of a routing tile, with each row's pair and point.
-struct SimtRows {
+// A block's 16 R rows: a part of a routing tile.
+template <int R> struct SimtRows {
     int expert, valid;
     int64_t row0;
     bool null_expert;
-    __device__ __forceinline__ bool load(const ExpRoute &rt, int64_t *tok, int64_t *pair) {
-        const int t = blockIdx.x >> 1, half = blockIdx.x & 1;
+    __device__ __forceinline__ bool load(const ExpRoute &rt) {
+        constexpr int kParts = 8 / R;
+        const int t = blockIdx.x / kParts, part = blockIdx.x % kParts;
         if (t >= rt.tiles()) return false;
         const auto x = rt.tile(t);
         expert = x.expert;
         null_expert = expert >= rt.K;
-        row0 = x.row0 + half * kB;
-        valid = x.valid - half * kB;
-        if (valid > kB) valid = kB;
-        if (valid <= 0) return false;
-        if (threadIdx.x < kB) {
-            const int m = threadIdx.x < valid ? threadIdx.x : 0;
-            const int64_t p = rt.pair(row0 + m);
-            pair[threadIdx.x] = p;
-            tok[threadIdx.x] = rt.token(p);
-        }
-        __syncthreads();
-        return true;
+        row0 = x.row0 + part * (16 * R);
+        valid = x.valid - part * (16 * R);
+        if (valid > 16 * R) valid = 16 * R;
+        return valid > 0;
+    }
+    // The pairs of this thread's rows: on their way while it multiplies, but
+    // with eight rows only after that (8 registers more than 128 cost the
+    // second block of an SM: 145 us against 119 for 8192 x 512 x 512).
+    static constexpr bool kEarly = R < 8;
+    __device__ __forceinline__ void own(const ExpRoute &rt, int (&pair)[R]) const {
+        const int m = (threadIdx.x >> 4) * R;
+#pragma unroll
+        for (int i = 0; i < R; ++i) pair[i] = m + i < valid ? (int)rt.pair(row0 + m + i) : 0;
     }
 };
 
@@ -207,21 +237,22 @@ __device__ __forceinline__ void store_result(const ExpCall &c, int64_t pair, int
 
 // First product: f(W1 x + b1) (gated: f(a) u) to the hidden rows, or, for
 // the linear form, to the result.
-template <typename T, int ACT, bool GATED, bool V>
+template <typename T, int ACT, bool GATED, bool V, int R>
 __global__ void __launch_bounds__(256) simt_first_kernel(ExpCall c) {
-    __shared__ __align__(16) SimtSmem sh;
-    __shared__ int64_t tok[kB], pair[kB];
-    SimtRows rows;
+    __shared__ __align__(16) SimtSmem<R> sh;
+    SimtRows<R> rows;
     exp_wait();
-    if (!rows.load(c.rt, tok, pair)) return;
+    if (!rows.load(c.rt)) return;
     const int d = c.s.d, width = c.s.mlp ? c.s.h : c.s.o, n0 = blockIdx.y * kB;
     const T *x = (const T *)c.x;
     if (rows.null_expert && c.s.mlp) return;
-    float acc[2][4][4];
-    zero(acc[0]);
-    zero(acc[1]);
+    int own[R] = {};
+    if (rows.kEarly && !c.s.mlp) rows.own(c.rt, own);
+    Acc<R> acc[2];
+    acc[0].zero();
+    acc[1].zero();
     if (!rows.null_expert) {
-        const GatherRows<T> la{x, tok, rows.valid, d};
+        const GatherRows<T> la{x, c.rt, rows.row0, rows.valid, d};
 #pragma unroll
         for (int half = 0; half < (GATED ? 2 : 1); ++half) {
             const T *w = (const T *)c.w1 + ((size_t)rows.expert * c.s.first() +
@@ -229,59 +260,64 @@ __global__ void __launch_bounds__(256) simt_first_kernel(ExpCall c) {
             simt_mma<V>(sh, acc[half], d, la, PlainRows<T>{w, n0, width, d});
         }
     }
+    if (!rows.kEarly && !c.s.mlp) rows.own(c.rt, own);
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const T *b = c.b1 ? (const T *)c.b1 + (size_t)rows.expert * c.s.first() : nullptr;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int m = ty * 4 + i;
+    for (int i = 0; i < R; ++i) {
+        const int m = ty * R + i;
         if (m >= rows.valid) continue;
+        const int64_t pair = own[i], tok = c.rt.token(pair);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int col = n0 + tx * 4 + j;
             if (col >= width) continue;
             float v = 0.f;
             if (!rows.null_expert) {
-                v = act_of<ACT>(acc[0][i][j] + (b ? value_at(b + col) : 0.f));
-                if (GATED) v *= acc[1][i][j] + (b ? value_at(b + width + col) : 0.f);
+                v = act_of<ACT>(acc[0].at(i, j) + (b ? value_at(b + col) : 0.f));
+                if (GATED) v *= acc[1].at(i, j) + (b ? value_at(b + width + col) : 0.f);
             }
             if (c.s.mlp)
                 ((float *)c.hid)[(rows.row0 + m) * width + col] = v;
             else
-                store_result<T>(c, pair[m], tok[m], col, v, rows.null_expert);
+                store_result<T>(c, pair, tok, col, v, rows.null_expert);
         }
     }
 }
 
 // Second product: W2 h + b2.
-template <typename T, bool V>
+template <typename T, bool V, int R>
 __global__ void __launch_bounds__(256) simt_second_kernel(ExpCall c) {
-    __shared__ __align__(16) SimtSmem sh;
-    __shared__ int64_t tok[kB], pair[kB];
-    SimtRows rows;
+    __shared__ __align__(16) SimtSmem<R> sh;
+    SimtRows<R> rows;
     exp_wait();
-    if (!rows.load(c.rt, tok, pair)) return;
+    if (!rows.load(c.rt)) return;
     const int h = c.s.h, o = c.s.o, n0 = blockIdx.y * kB;
     const float *hid = (const float *)c.hid;
-    float acc[4][4];
-    zero(acc);
+    int own[R];
+    if (rows.kEarly) rows.own(c.rt, own);
+    Acc<R> acc;
+    acc.zero();
     if (!rows.null_expert) {
         const T *w = (const T *)c.w2 + (size_t)rows.expert * o * h;
         simt_mma<V>(sh, acc, h, PlainRows<float>{hid + rows.row0 * h, 0, rows.valid, h},
                     PlainRows<T>{w, n0, o, h});
     }
+    if (!rows.kEarly) rows.own(c.rt, own);
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int m = ty * 4 + i;
+    for (int i = 0; i < R; ++i) {
+        const int m = ty * R + i;
         if (m >= rows.valid) continue;
+        const int64_t pair = own[i], tok = c.rt.token(pair);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int col = n0 + tx * 4 + j;
             if (col >= o) continue;
-            float v = acc[i][j];
+            float v = acc.at(i, j);
             if (c.b2 && !rows.null_expert)
                 v += value_at((const T *)c.b2 + (size_t)rows.expert * o + col);
-            store_result<T>(c, pair[m], tok[m], col, v, rows.null_expert);
+            store_result<T>(c, pair, tok, col, v, rows.null_expert);
         }
     }
 }
@@ -290,48 +326,49 @@ __global__ void __launch_bounds__(256) simt_second_kernel(ExpCall c) {
 // the hidden gradient (mlp: q = W2^T dy; linear: dy itself), and writes
 // da = d loss / d (W1 x + b1), resp * h for dW2, and this block's part of
 // dresp = <q, h> (mlp) or <dy, f(z)> (linear).
-template <typename T, int ACT, bool GATED, bool V>
+template <typename T, int ACT, bool GATED, bool V, int R>
 __global__ void __launch_bounds__(256) simt_da_kernel(ExpCall c) {
-    __shared__ __align__(16) SimtSmem sh;
-    __shared__ int64_t tok[kB], pair[kB];
-    SimtRows rows;
+    __shared__ __align__(16) SimtSmem<R> sh;
+    SimtRows<R> rows;
     exp_wait();
-    if (!rows.load(c.rt, tok, pair) || rows.null_expert) return;
+    if (!rows.load(c.rt) || rows.null_expert) return;
     const int d = c.s.d, o = c.s.o, width = c.s.mlp ? c.s.h : c.s.o, n0 = blockIdx.y * kB;
     const T *x = (const T *)c.x, *dy = (const T *)c.dy;
-    float acc[2][4][4], q[4][4];
-    zero(acc[0]);
-    zero(acc[1]);
-    zero(q);
+    int own[R];
+    rows.own(c.rt, own);
+    Acc<R> acc[2], q;
+    acc[0].zero();
+    acc[1].zero();
+    q.zero();
 #pragma unroll
     for (int half = 0; half < (GATED ? 2 : 1); ++half) {
         const T *w = (const T *)c.w1 + ((size_t)rows.expert * c.s.first() +
                                         (size_t)half * width) * d;
-        simt_mma<V>(sh, acc[half], d, GatherRows<T>{x, tok, rows.valid, d},
+        simt_mma<V>(sh, acc[half], d, GatherRows<T>{x, c.rt, rows.row0, rows.valid, d},
                     PlainRows<T>{w, n0, width, d});
     }
     if (c.s.mlp) {
         const T *w = (const T *)c.w2 + (size_t)rows.expert * o * width;
-        simt_mma<V>(sh, q, o, GatherRows<T>{dy, tok, rows.valid, o}, PlainCols<T>{w, n0, width});
+        simt_mma<V>(sh, q, o, GatherRows<T>{dy, c.rt, rows.row0, rows.valid, o}, PlainCols<T>{w, n0, width});
     }
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const T *b = c.b1 ? (const T *)c.b1 + (size_t)rows.expert * c.s.first() : nullptr;
     float *da = (float *)c.da, *hs = (float *)c.hid;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int m = ty * 4 + i;
+    for (int i = 0; i < R; ++i) {
+        const int m = ty * R + i;
         const bool ok = m < rows.valid;
-        const int64_t row = rows.row0 + m;
+        const int64_t row = rows.row0 + m, pair = own[i], tok = c.rt.token(pair);
+        const float g = ok && c.resp ? c.resp[pair] : 1.f;
         float part = 0.f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int col = n0 + tx * 4 + j;
             if (!ok || col >= width) continue;
-            const float g = c.resp ? c.resp[pair[m]] : 1.f;
             float f, df;
-            act_both<ACT>(acc[0][i][j] + (b ? value_at(b + col) : 0.f), f, df);
-            const float up = GATED ? acc[1][i][j] + (b ? value_at(b + width + col) : 0.f) : 1.f;
-            const float qq = c.s.mlp ? q[i][j] : value_at(dy + tok[m] * o + col);
+            act_both<ACT>(acc[0].at(i, j) + (b ? value_at(b + col) : 0.f), f, df);
+            const float up = GATED ? acc[1].at(i, j) + (b ? value_at(b + width + col) : 0.f) : 1.f;
+            const float qq = c.s.mlp ? q.at(i, j) : value_at(dy + tok * o + col);
             part = fmaf(qq, f * up, part);
             da[row * c.s.first() + col] = g * qq * up * df;
             if (GATED) da[row * c.s.first() + width + col] = g * qq * f;
@@ -340,40 +377,43 @@ __global__ void __launch_bounds__(256) simt_da_kernel(ExpCall c) {
         // the 16 lanes of a row
 #pragma unroll
         for (int s = 8; s; s >>= 1) part += __shfl_xor_sync(0xffffffffu, part, s);
-        if (tx == 0 && ok && c.dresp) c.rpart[pair[m] * c.nrpart + blockIdx.y] = part;
+        if (tx == 0 && ok && c.dresp) c.rpart[pair * c.nrpart + blockIdx.y] = part;
     }
 }
 
 // dx (or its per-pair part) = da W1.
-template <typename T, bool V>
+template <typename T, bool V, int R>
 __global__ void __launch_bounds__(256) simt_dx_kernel(ExpCall c) {
-    __shared__ __align__(16) SimtSmem sh;
-    __shared__ int64_t tok[kB], pair[kB];
-    SimtRows rows;
+    __shared__ __align__(16) SimtSmem<R> sh;
+    SimtRows<R> rows;
     exp_wait();
-    if (!rows.load(c.rt, tok, pair)) return;
+    if (!rows.load(c.rt)) return;
     const int d = c.s.d, first = c.s.first(), n0 = blockIdx.y * kB;
     const float *da = (const float *)c.da;
-    float acc[4][4];
-    zero(acc);
+    int own[R];
+    if (rows.kEarly) rows.own(c.rt, own);
+    Acc<R> acc;
+    acc.zero();
     if (!rows.null_expert) {
         const T *w = (const T *)c.w1 + (size_t)rows.expert * first * d;
         simt_mma<V>(sh, acc, first, PlainRows<float>{da + rows.row0 * first, 0, rows.valid, first},
                     PlainCols<T>{w, n0, d});
     }
+    if (!rows.kEarly) rows.own(c.rt, own);
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int m = ty * 4 + i;
+    for (int i = 0; i < R; ++i) {
+        const int m = ty * R + i;
         if (m >= rows.valid) continue;
+        const int64_t pair = own[i], tok = c.rt.token(pair);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int col = n0 + tx * 4 + j;
             if (col >= d) continue;
             if (c.s.direct())
-                ((T *)c.dx)[tok[m] * d + col] = from_float<T>(acc[i][j]);
+                ((T *)c.dx)[tok * d + col] = from_float<T>(acc.at(i, j));
             else
-                c.slots[pair[m] * d + col] = acc[i][j];
+                c.slots[pair * d + col] = acc.at(i, j);
         }
     }
 }
@@ -383,8 +423,9 @@ __global__ void __launch_bounds__(256) simt_dx_kernel(ExpCall c) {
 // A = da, B = x (gathered).
 template <typename T, bool SECOND, bool V>
 __global__ void __launch_bounds__(256) simt_dw_kernel(ExpCall c, int mtiles) {
-    __shared__ __align__(16) SimtSmem sh;
-    const int e = blockIdx.x / mtiles, m0 = (blockIdx.x % mtiles) * kB, n0 = blockIdx.y * kB;
+    __shared__ __align__(16) SimtSmem<4> sh;
+    constexpr int R = 4;
+    const int e = blockIdx.x / mtiles, m0 = (blockIdx.x % mtiles) * (16 * R), n0 = blockIdx.y * kB;
     const int M = SECOND ? c.s.o : c.s.first(), N = SECOND ? c.s.h : c.s.d;
     exp_wait();
     const int64_t row0 = c.rt.ids ? c.rt.seg[e] : 0;
@@ -392,8 +433,8 @@ __global__ void __launch_bounds__(256) simt_dw_kernel(ExpCall c, int mtiles) {
     const float *own = (const float *)(SECOND ? c.hid : c.da);
     const T *points = (const T *)(SECOND ? c.dy : c.x);
     const int pw = SECOND ? c.s.o : c.s.d, ow = SECOND ? c.s.h : c.s.first();
-    float acc[4][4];
-    zero(acc);
+    Acc<R> acc;
+    acc.zero();
     const PointCols<T> pc{points, c.rt, row0, SECOND ? m0 : n0, pw};
     const PlainCols<float> oc{own + row0 * ow, SECOND ? n0 : m0, ow};
     if constexpr (SECOND) simt_mma<V>(sh, acc, cnt, pc, oc);
@@ -401,43 +442,83 @@ __global__ void __launch_bounds__(256) simt_dw_kernel(ExpCall c, int mtiles) {
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     T *out = (T *)(SECOND ? c.dw2 : c.dw1) + (size_t)e * M * N;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int m = m0 + ty * 4 + i;
+    for (int i = 0; i < R; ++i) {
+        const int m = m0 + ty * R + i;
         if (m >= M) continue;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int n = n0 + tx * 4 + j;
             if (n >= N) continue;
-            out[(size_t)m * N + n] = from_float<T>(acc[i][j]);
+            out[(size_t)m * N + n] = from_float<T>(acc.at(i, j));
         }
     }
 }
 
-static unsigned tiles_of(int64_t n) { return (unsigned)((n + kB - 1) / kB); }
+static int64_t tiles_of(int64_t n, int w) { return (n + w - 1) / w; }
+
+// Rows per thread of a product over the points' rows, with `cols` column
+// tiles: the most that the experts' segments fill and that leaves every SM
+// work.  8 against 4: 238 us against 266 for 8192 pairs of 8 experts 512-512-512;
+// with 64 pairs an expert 256 against 228, with 144 blocks 57 against 52.  2
+// against 4: 125 us against 142 with 9 pairs an expert, 266 against 228 with 64.
+// What keeps two or three arrays of sums (da) lost with 8 (312 us against 286:
+// one block an SM), and so did the weight gradients (235 against 185: the
+// experts' lengths differ, and large tiles even them out less).
+static int rows_per_thread(const ExpShape &p, int64_t cols) {
+    const int64_t mean = p.P / p.K;
+    if (mean <= 32) return 2;
+    return mean >= 128 && tiles_of(p.P, 128) * cols >= 3 * kSms / 2 ? 8 : 4;
+}
+
+// fn(integral_constant<R>) for R = min(r, MAX); odd widths and the 16-bit
+// types (which come here only where they are forced to) always take 4.
+template <bool V, int MAX, class F> static cudaError_t with_rows(int r, F fn) {
+    if constexpr (V) {
+        if constexpr (MAX == 8)
+            if (r == 8) return fn(std::integral_constant<int, 8>());
+        if (r == 2) return fn(std::integral_constant<int, 2>());
+    }
+    return fn(std::integral_constant<int, 4>());
+}
 
 template <typename T, int ACT, bool GATED, bool V>
 static cudaError_t simt_products(const ExpCall &c, bool backward, cudaStream_t s) {
     const ExpShape &p = c.s;
-    const unsigned rows = 2u * (unsigned)c.rt.max_tiles;
     const int width = p.mlp ? p.h : p.o;
+    // a product over the points' rows, with n columns
+    const auto rows = [&](auto most, int n, auto launch) {
+        const unsigned cols = (unsigned)tiles_of(n, kB);
+        return with_rows<V, most()>(rows_per_thread(p, cols), [&](auto r) {
+            return launch(r, dim3(8u / r() * (unsigned)c.rt.max_tiles, cols));
+        });
+    };
+    const std::integral_constant<int, 4> four;
+    const std::integral_constant<int, 8> eight;
     cudaError_t e;
     if (!backward) {
-        e = exp_launch(simt_first_kernel<T, ACT, GATED, V>, dim3(rows, tiles_of(width)), 256, 0, s,
-                       c);
+        e = rows(eight, width, [&](auto r, dim3 g) {
+            return exp_launch(simt_first_kernel<T, ACT, GATED, V, r()>, g, 256, 0, s, c);
+        });
         if (e == cudaSuccess && p.mlp)
-            e = exp_launch(simt_second_kernel<T, V>, dim3(rows, tiles_of(p.o)), 256, 0, s, c);
+            e = rows(eight, p.o, [&](auto r, dim3 g) {
+                return exp_launch(simt_second_kernel<T, V, r()>, g, 256, 0, s, c);
+            });
         return e;
     }
-    e = exp_launch(simt_da_kernel<T, ACT, GATED, V>, dim3(rows, tiles_of(width)), 256, 0, s, c);
+    e = rows(four, width, [&](auto r, dim3 g) {
+        return exp_launch(simt_da_kernel<T, ACT, GATED, V, r()>, g, 256, 0, s, c);
+    });
     if (e == cudaSuccess)
-        e = exp_launch(simt_dx_kernel<T, V>, dim3(rows, tiles_of(p.d)), 256, 0, s, c);
-    const unsigned m1 = tiles_of(p.first()), m2 = tiles_of(p.o);
+        e = rows(eight, p.d, [&](auto r, dim3 g) {
+            return exp_launch(simt_dx_kernel<T, V, r()>, g, 256, 0, s, c);
+        });
+    const unsigned m1 = (unsigned)tiles_of(p.first(), kB), m2 = (unsigned)tiles_of(p.o, kB);
     if (e == cudaSuccess)
-        e = exp_launch(simt_dw_kernel<T, false, V>, dim3(m1 * p.K, tiles_of(p.d)), 256, 0, s, c,
-                       (int)m1);
+        e = exp_launch(simt_dw_kernel<T, false, V>, dim3(m1 * p.K, (unsigned)tiles_of(p.d, kB)),
+                       256, 0, s, c, (int)m1);
     if (e == cudaSuccess && p.mlp)
-        e = exp_launch(simt_dw_kernel<T, true, V>, dim3(m2 * p.K, tiles_of(p.h)), 256, 0, s, c,
-                       (int)m2);
+        e = exp_launch(simt_dw_kernel<T, true, V>, dim3(m2 * p.K, (unsigned)tiles_of(p.h, kB)),
+                       256, 0, s, c, (int)m2);
     return e;
 }
 
