@@ -349,7 +349,8 @@ __global__ void __launch_bounds__(256) simt_da_kernel(ExpCall c) {
     }
     if (c.s.mlp) {
         const T *w = (const T *)c.w2 + (size_t)rows.expert * o * width;
-        simt_mma<V>(sh, q, o, GatherRows<T>{dy, c.rt, rows.row0, rows.valid, o}, PlainCols<T>{w, n0, width});
+        simt_mma<V>(sh, q, o, GatherRows<T>{dy, c.rt, rows.row0, rows.valid, o},
+                    PlainCols<T>{w, n0, width});
     }
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const T *b = c.b1 ? (const T *)c.b1 + (size_t)rows.expert * c.s.first() : nullptr;

@@ -304,6 +304,18 @@ def test_mlp(N, d, h, o, K, r, dtype, activation, gated, opt, flags):
     check(inputs(N + d + h, N, d, h, o, K, r, dtype, gated=gated, **opt), activation, gated, flags)
 
 
+@pytest.mark.parametrize("N,d,h,o,K,r,gated,opt", [
+    (1700, 64, 0, 1160, 1, 0, False, {"res": True}),          # 8 rows a thread, 14 x 19 tiles
+    (1650, 36, 40, 560, 3, 2, True, {"cut": 0.1}),            # 26 x 9, segments of unequal length
+    (1650, 560, 0, 24, 4, 2, False, {"cut": 0.4, "res": True}),   # the points' gradient
+    (1700, 563, 0, 21, 1, 0, False, {}),                      # odd widths
+    (90, 40, 72, 24, 7, 2, True, {"cut": 0.3, "res": True}),  # 2 rows a thread
+])
+def test_fp32_rows_a_thread(N, d, h, o, K, r, gated, opt):
+    use = [0, 0, 0, 1, 2, 2, K - 1] if K > 2 else None        # lengths differ
+    check(inputs(21, N, d, h, o, K, r, "f32", gated, use=use, **opt), "silu", gated)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("gated", [False, True])
 def test_relu_with_whole_numbers(dtype, gated):
