@@ -24,6 +24,12 @@
 // contiguous axis reads it K-major, one over its rows (the weights in the
 // backward pass, all operands of the weight gradients) MN-major, so nothing
 // is transposed.
+//
+// Bound, at 8192 points, 2 of 16 gated experts 2048-4096-2048 in bf16: first and
+// second together 640 us (1290 TFLOP/s: a stage's 64 KB a pair from L2 take 50
+// of its 64 bytes a clock), dx 420 us, dw1 460, dw2 233 (1400 TFLOP/s, the power
+// cap), da 778 (1060 TFLOP/s: 128-column products for q need 96 bytes a clock).
+// Contractions of one or two stages (128 columns) are bound by the epilogue.
 #include "experts.h"
 #include "tc_ptx.cuh"
 #include "tensor_map.h"

@@ -531,6 +531,33 @@ def test_repeats_are_bitwise_equal(N):
     assert torch.equal(y0, y2)
 
 
+@pytest.mark.parametrize("N,d,h,o,K,r,dtype,gated", [
+    (300, 64, 72, 136, 6, 2, "bf16", True),       # segments end inside tiles
+    (900, 64, 0, 264, 2, 1, "f16", False),        # pairs of row tiles
+    (130, 33, 21, 65, 5, 3, "bf16", False),       # padded copies
+    (300, 64, 72, 136, 1, 0, "f16", True),
+    (4, 64, 72, 136, 6, 2, "bf16", True),         # few points forward
+    (300, 40, 72, 136, 6, 2, "f32", True),
+    (5000, 40, 24, 16, 60, 1, "f32", False),      # counting sort in steps
+])
+def test_contents_of_the_workspace_do_not_matter(N, d, h, o, K, r, dtype, gated):
+    """Only its error word has to be clear: the rest may hold NaNs."""
+    use = list(range(K - 1)) or None              # an expert that nobody uses
+    s = cuda(inputs(13, N, d, h, o, K, r, dtype, gated, cut=0.2 if r else 0.0, use=use))
+    ws = workspace(s, gated, True)
+    ws.view.zero_()
+    y0, _ = forward(s, "silu", gated, ws=ws)
+    ws.view.zero_()
+    g0, _ = backward(s, "silu", gated, ws=ws)
+    for run in (lambda: ({"y": forward(s, "silu", gated, ws=ws)[0]}, {"y": y0}),
+                lambda: (backward(s, "silu", gated, ws=ws)[0], g0)):
+        ws.view[256:] = 255
+        got, want = run()
+        assert gmm.gmm_last_error(ws) == 0
+        for k in want:
+            assert torch.equal(got[k], want[k]) and got[k].isfinite().all(), k
+
+
 @pytest.mark.parametrize("N", [3, 200])
 def test_captured_calls(N):
     """Two captured graphs with a workspace each, replayed in turn on new
