@@ -409,7 +409,9 @@ gmm_status kmeans_step(const void *X, gmm_dtype dtype, int B, int64_t N, int d, 
  * Without ids (NULL, r = 0, K = 1) every point passes through the one map:
  * a dense layer, f(X W^T + b) + residual.
  *
- * Sums are fp32 (tensor-core accumulators, or FMA).  Results are rounded to
+ * Sums are fp32 (FMA, or tensor-core accumulators, which truncate: dresp, the
+ * one fp32 result of a 16-bit call, is within 6e-6 of its 2-norm after
+ * contractions over 2048, where FMA is within 7e-7).  Results are rounded to
  * `dtype` once; for 16-bit types the hidden vector h and, in the backward
  * pass, the gradients of the pre-activations and g h are rounded to `dtype`
  * as well, because they are operands of the next tensor-core product.  Every

@@ -198,7 +198,8 @@ def expert_linear_backward(dY, X, ids, resp, W, b, ws: Workspace, activation: st
     c.rows(dY, "dY", c.o)
     with c:
         dX, dW, db, dresp = _like(X), _like(W), _like(b), _like(resp)
-        c.run("gmm_expert_linear_backward", _lib.load().gmm_expert_linear_backward, flags, dY, X, ids, resp, W, b, dX, dW, db, dresp)
+        c.run("gmm_expert_linear_backward", _lib.load().gmm_expert_linear_backward, flags, dY, X,
+              ids, resp, W, b, dX, dW, db, dresp)
     return dX, dW, db, dresp
 
 
