@@ -1,7 +1,8 @@
 // The experts' products on CUDA cores, for fp32 and for widths or pointers
 // the tensor-core kernels do not take.  Every product is a tile of 16 R x 64
-// with an R x 4 micro tile per thread, fp32 throughout; what one product hands
-// to the next stays fp32 in the workspace.  Bound by the FMA pipes and what
+// with an R x 4 micro tile per thread (forward calls of a few rows per expert: a
+// dot product per warp), fp32 throughout; what one product hands to the next
+// stays fp32 in the workspace.  Bound by the FMA pipes and what
 // feeds them from shared memory: 35 TFLOP/s at 4096 x 512 x 512 (R = 8; 30 with
 // R = 4, 23 with R = 2), 25 in a backward pass of 8192 pairs of 512-512-512.
 #include <type_traits>
@@ -322,6 +323,105 @@ __global__ void __launch_bounds__(256) simt_second_kernel(ExpCall c) {
     }
 }
 
+// ----------------------------------------------- few rows per expert, forward
+// sums[i] = sum_k A(m0 + i, k) w[k] for kFewRows rows, by one warp along k, in
+// every lane.  Rows past the segment are NULL and give 0.
+constexpr int kFewRows = 4;
+template <bool VEC, class A, typename T>
+__device__ __forceinline__ void dots(float (&sums)[kFewRows], const A &opa, int m0, int K,
+                                     const T *w) {
+    const int lane = threadIdx.x & 31;
+    const typename A::E *a[kFewRows];
+#pragma unroll
+    for (int i = 0; i < kFewRows; ++i) {
+        a[i] = opa.row(m0 + i);
+        sums[i] = 0.f;
+    }
+    if constexpr (VEC) {
+#pragma unroll 4
+        for (int k = lane * 4; k < K; k += 128) {
+            const float4 b = *reinterpret_cast<const float4 *>(w + k);
+#pragma unroll
+            for (int i = 0; i < kFewRows; ++i)
+                if (a[i]) {
+                    const float4 v = *reinterpret_cast<const float4 *>(a[i] + k);
+                    sums[i] = fmaf(v.x, b.x, sums[i]);
+                    sums[i] = fmaf(v.y, b.y, sums[i]);
+                    sums[i] = fmaf(v.z, b.z, sums[i]);
+                    sums[i] = fmaf(v.w, b.w, sums[i]);
+                }
+        }
+    } else {
+#pragma unroll 4
+        for (int k = lane; k < K; k += 32) {
+            const float b = value_at(w + k);
+#pragma unroll
+            for (int i = 0; i < kFewRows; ++i)
+                if (a[i]) sums[i] = fmaf(value_at(a[i] + k), b, sums[i]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kFewRows; ++i)
+#pragma unroll
+        for (int o = 16; o; o >>= 1) sums[i] += __shfl_xor_sync(0xffffffffu, sums[i], o);
+}
+
+// One layer where the experts' segments hold few rows: a warp takes one output
+// column, reads that row of the weight once, coalesced, and multiplies it with
+// four points' rows at a time (from L1: the block's eight warps share them).
+// Bound by the weights' read for a row or two, then by L1.
+template <typename T, int ACT, bool GATED, bool SECOND, bool V>
+__global__ void __launch_bounds__(256) simt_few_kernel(ExpCall c) {
+    exp_wait();
+    SimtRows<8> rows;
+    const int n = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int width = c.s.mlp && !SECOND ? c.s.h : c.s.o;
+    if (!rows.load(c.rt) || n >= width) return;
+    const bool last = SECOND || !c.s.mlp;
+    if (rows.null_expert && !last) return;
+    const int depth = SECOND ? c.s.h : c.s.d, first = SECOND ? c.s.o : c.s.first();
+    const size_t at = (size_t)rows.expert * first + n;
+    const T *w = (const T *)(SECOND ? c.w2 : c.w1) + at * depth;
+    const T *b = (const T *)(SECOND ? c.b2 : c.b1);
+    for (int m0 = 0; m0 < rows.valid; m0 += kFewRows) {
+        float z[kFewRows] = {}, u[kFewRows] = {};
+        if (!rows.null_expert) {
+            if constexpr (SECOND) {
+                const PlainRows<float> a{(const float *)c.hid + rows.row0 * depth, 0, rows.valid,
+                                         depth};
+                dots<V>(z, a, m0, depth, w);
+            } else {
+                const GatherRows<T> a{(const T *)c.x, c.rt, rows.row0, rows.valid, depth};
+                dots<V>(z, a, m0, depth, w);
+                if constexpr (GATED) dots<V>(u, a, m0, depth, w + (size_t)width * depth);
+            }
+        }
+        // row m0 + i in lane i
+        float v = z[0], up = u[0];
+#pragma unroll
+        for (int i = 1; i < kFewRows; ++i)
+            if (lane == i) {
+                v = z[i];
+                up = u[i];
+            }
+        const int m = m0 + lane;
+        if (lane >= kFewRows || m >= rows.valid) continue;
+        if (!rows.null_expert) {
+            if (b) v += value_at(b + at);
+            if constexpr (!SECOND) {
+                v = act_of<ACT>(v);
+                if constexpr (GATED) v *= up + (b ? value_at(b + at + width) : 0.f);
+            }
+        }
+        if (last) {
+            const int64_t pair = c.rt.pair(rows.row0 + m);
+            store_result<T>(c, pair, c.rt.token(pair), n, v, rows.null_expert);
+        } else {
+            ((float *)c.hid)[(rows.row0 + m) * width + n] = v;
+        }
+    }
+}
+
 // Backward, up to the first layer's pre-activations: recomputes them, forms
 // the hidden gradient (mlp: q = W2^T dy; linear: dy itself), and writes
 // da = d loss / d (W1 x + b1), resp * h for dW2, and this block's part of
@@ -457,6 +557,12 @@ __global__ void __launch_bounds__(256) simt_dw_kernel(ExpCall c, int mtiles) {
 
 static int64_t tiles_of(int64_t n, int w) { return (n + w - 1) / w; }
 
+// Mean rows per expert up to which a forward call takes simt_few_kernel.  One
+// dense 1024-4096 map: 1 point 4.9 us against 52 in tiles, 8 points 10 against
+// 53; 16 points, r = 4 of 64 experts 512-1024-512 67 against 176; with 9 rows
+// an expert (300 points, r = 2 of 64 experts 512-512-512) 137 against 125.
+constexpr int64_t kFewMean = 8;
+
 // Rows per thread of a product over the points' rows, with `cols` column
 // tiles: the most that the experts' segments fill and that leaves every SM
 // work.  8 against 4: 238 us against 266 for 8192 pairs of 8 experts 512-512-512;
@@ -496,6 +602,17 @@ static cudaError_t simt_products(const ExpCall &c, bool backward, cudaStream_t s
     const std::integral_constant<int, 4> four;
     const std::integral_constant<int, 8> eight;
     cudaError_t e;
+    if constexpr (sizeof(T) == 4)
+        if (!backward && p.P <= kFewMean * (int64_t)p.K) {
+            const auto grid = [&](int n) {
+                return dim3((unsigned)c.rt.max_tiles, (unsigned)tiles_of(n, 8));
+            };
+            e = exp_launch(simt_few_kernel<T, ACT, GATED, false, V>, grid(width), 256, 0, s, c);
+            if (e == cudaSuccess && p.mlp)
+                e = exp_launch(simt_few_kernel<T, GMM_ACT_NONE, false, true, V>, grid(p.o), 256, 0,
+                               s, c);
+            return e;
+        }
     if (!backward) {
         e = rows(eight, width, [&](auto r, dim3 g) {
             return exp_launch(simt_first_kernel<T, ACT, GATED, V, r()>, g, 256, 0, s, c);

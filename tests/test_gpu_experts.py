@@ -316,6 +316,19 @@ def test_fp32_rows_a_thread(N, d, h, o, K, r, gated, opt):
     check(inputs(21, N, d, h, o, K, r, "f32", gated, use=use, **opt), "silu", gated)
 
 
+@pytest.mark.parametrize("N,d,h,o,K,r,gated,opt", [
+    (1, 1024, 0, 520, 1, 0, False, {"res": True}),
+    (8, 36, 20, 12, 1, 0, True, {}),                          # two groups of four rows
+    (1, 64, 136, 72, 12, 8, True, {"res": True}),
+    (40, 64, 40, 24, 11, 2, False, {"cut": 0.5, "res": True}),    # points without any
+    (30, 64, 0, 24, 5, 1, False, {"cut": 0.5, "resp": False}),
+    (29, 33, 21, 65, 9, 2, True, {"cut": 0.2}),               # odd widths
+    (150, 40, 24, 16, 40, 2, False, {"use": [0, 0, 0, 39]}),  # one expert has most of the rows
+])
+def test_fp32_few_rows(N, d, h, o, K, r, gated, opt):
+    check(inputs(22, N, d, h, o, K, r, "f32", gated, **opt), "gelu", gated)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("gated", [False, True])
 def test_relu_with_whole_numbers(dtype, gated):
