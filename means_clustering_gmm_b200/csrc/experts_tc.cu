@@ -505,6 +505,9 @@ __global__ void __launch_bounds__(kThreads, 1) exp_tc_kernel(const __grid_consta
                 if (c.resp) g = c.resp[pair];
             }
             if constexpr (C::kBias) {
+                // every lane has read the biases of the tile before: its
+                // columns end in branches, behind which nothing else says so
+                __syncwarp();
                 const T *b = (const T *)(KIND == kSecond ? c.b2 : c.b1);
                 if (b && !none) b += (size_t)j.expert * (KIND == kSecond ? s.o : s.first());
 #pragma unroll
