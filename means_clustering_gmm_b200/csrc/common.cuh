@@ -22,13 +22,13 @@ __device__ __forceinline__ void set_error(int *err, int code) {
 __device__ __forceinline__ float to_float(float v) { return v; }
 __device__ __forceinline__ float to_float(__half v) { return __half2float(v); }
 __device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
-template <typename T> __device__ __forceinline__ float load_elem(const T *p);
-template <> __device__ __forceinline__ float load_elem<float>(const float *p) { return __ldg(p); }
-template <> __device__ __forceinline__ float load_elem<__half>(const __half *p) {
-    return __half2float(__ldg(p));
-}
-template <> __device__ __forceinline__ float load_elem<__nv_bfloat16>(const __nv_bfloat16 *p) {
-    return __bfloat162float(__ldg(p));
+// One element, by an ordinary load: the compiler keeps it behind the test that
+// guards it.  It need not do so with __ldg of the 16-bit types, whose inline
+// assembly it takes to have no effects: a load guarded by `p < N` or by a
+// pointer's test may then move above the test and read what is not there (a
+// kernel that read a bias of address 0 this way faulted).
+template <typename T> __device__ __forceinline__ float load_elem(const T *p) {
+    return to_float(*p);
 }
 
 // Per-point selection of the best components (soft assignment): a

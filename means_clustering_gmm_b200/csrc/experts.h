@@ -181,11 +181,6 @@ template <int ACT> __device__ __forceinline__ float act_fast(float z) {
     return f.x;
 }
 
-// An ordinary load: the compiler keeps it behind the test that guards it,
-// which it need not do with the inline assembly behind __ldg of 16-bit types.
-template <typename T> __device__ __forceinline__ float value_at(const T *p) {
-    return to_float(*p);
-}
 template <typename T> __device__ __forceinline__ T from_float(float v);
 template <> __device__ __forceinline__ float from_float<float>(float v) { return v; }
 template <> __device__ __forceinline__ __half from_float<__half>(float v) {

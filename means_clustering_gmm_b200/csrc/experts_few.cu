@@ -299,8 +299,8 @@ __global__ void __launch_bounds__(kThreads, 4) few_first_kernel(ExpCall c) {
     const int k0 = chunks * ks / KS * 32, k1 = min(chunks * (ks + 1) / KS * 32, s.d);
     // (the biases of the row this thread finishes, on their way meanwhile)
     const int own = min(n0 + (int)threadIdx.x % rows, width - 1);
-    const float bias = b ? value_at(b + own) : 0.f;
-    const float bias_up = GATED && b ? value_at(b + width + own) : 0.f;
+    const float bias = b ? load_elem(b + own) : 0.f;
+    const float bias_up = GATED && b ? load_elem(b + width + own) : 0.f;
     for (int col0 = 0; col0 < total; col0 += kCols) {
         const int cols = min(total - col0, kCols);
         float acc[4][4];
@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 3) few_second_kernel(ExpCall c, int 
                 const int id = s.dense ? 0 : c.rt.ids[q];
                 if (id >= 0 && id < s.K)
                     v = fmaf(c.resp ? c.resp[q] : 1.f,
-                             value_at((const T *)c.b2 + (size_t)id * s.o + out), v);
+                             load_elem((const T *)c.b2 + (size_t)id * s.o + out), v);
             }
         const size_t y = (size_t)tok * s.o + out;
         if (c.res) v += to_float(((const T *)c.res)[y]);

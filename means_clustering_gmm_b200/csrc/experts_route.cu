@@ -492,7 +492,7 @@ exp_colsum_kernel(ExpCall c, int w1, int w2) {
 #pragma unroll 4
         for (int64_t row = beg + ty; row < end; row += 8) {
             const int64_t p = rt.pair(row);
-            acc = fmaf(c.resp ? c.resp[p] : 1.f, value_at(dy + rt.token(p) * width + col), acc);
+            acc = fmaf(c.resp ? c.resp[p] : 1.f, load_elem(dy + rt.token(p) * width + col), acc);
         }
     } else if (col < width) {
         const float *da = (const float *)c.da;

@@ -102,11 +102,11 @@ template <class OP, int W, bool VEC> struct Part {
                 r[4 * i + 3] = v.w;
             } else if constexpr (OP::KROW) {
                 const int64_t k = k0 + (tid & 31);
-                r[i] = p[i] && k < K ? value_at(p[i] + k) : 0.f;
+                r[i] = p[i] && k < K ? load_elem(p[i] + k) : 0.f;
             } else {
                 const int64_t k = k0 + tid / kCols + 256 / kCols * i;
                 const int n = tid % kCols;
-                r[i] = k < K && n < op.cols() ? value_at(op.row(k) + n) : 0.f;
+                r[i] = k < K && n < op.cols() ? load_elem(op.row(k) + n) : 0.f;
             }
         }
     }
@@ -275,8 +275,8 @@ __global__ void __launch_bounds__(256) simt_first_kernel(ExpCall c) {
             if (col >= width) continue;
             float v = 0.f;
             if (!rows.null_expert) {
-                v = act_of<ACT>(acc[0].at(i, j) + (b ? value_at(b + col) : 0.f));
-                if (GATED) v *= acc[1].at(i, j) + (b ? value_at(b + width + col) : 0.f);
+                v = act_of<ACT>(acc[0].at(i, j) + (b ? load_elem(b + col) : 0.f));
+                if (GATED) v *= acc[1].at(i, j) + (b ? load_elem(b + width + col) : 0.f);
             }
             if (c.s.mlp)
                 ((float *)c.hid)[(rows.row0 + m) * width + col] = v;
@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(256) simt_second_kernel(ExpCall c) {
             if (col >= o) continue;
             float v = acc.at(i, j);
             if (c.b2 && !rows.null_expert)
-                v += value_at((const T *)c.b2 + (size_t)rows.expert * o + col);
+                v += load_elem((const T *)c.b2 + (size_t)rows.expert * o + col);
             store_result<T>(c, pair, tok, col, v, rows.null_expert);
         }
     }
@@ -354,10 +354,10 @@ __device__ __forceinline__ void dots(float (&sums)[kFewRows], const A &opa, int 
     } else {
 #pragma unroll 4
         for (int k = lane; k < K; k += 32) {
-            const float b = value_at(w + k);
+            const float b = load_elem(w + k);
 #pragma unroll
             for (int i = 0; i < kFewRows; ++i)
-                if (a[i]) sums[i] = fmaf(value_at(a[i] + k), b, sums[i]);
+                if (a[i]) sums[i] = fmaf(load_elem(a[i] + k), b, sums[i]);
         }
     }
 #pragma unroll
@@ -407,10 +407,10 @@ __global__ void __launch_bounds__(256) simt_few_kernel(ExpCall c) {
         const int m = m0 + lane;
         if (lane >= kFewRows || m >= rows.valid) continue;
         if (!rows.null_expert) {
-            if (b) v += value_at(b + at);
+            if (b) v += load_elem(b + at);
             if constexpr (!SECOND) {
                 v = act_of<ACT>(v);
-                if constexpr (GATED) v *= up + (b ? value_at(b + at + width) : 0.f);
+                if constexpr (GATED) v *= up + (b ? load_elem(b + at + width) : 0.f);
             }
         }
         if (last) {
@@ -467,9 +467,9 @@ __global__ void __launch_bounds__(256) simt_da_kernel(ExpCall c) {
             const int col = n0 + tx * 4 + j;
             if (!ok || col >= width) continue;
             float f, df;
-            act_both<ACT>(acc[0].at(i, j) + (b ? value_at(b + col) : 0.f), f, df);
-            const float up = GATED ? acc[1].at(i, j) + (b ? value_at(b + width + col) : 0.f) : 1.f;
-            const float qq = c.s.mlp ? q.at(i, j) : value_at(dy + tok * o + col);
+            act_both<ACT>(acc[0].at(i, j) + (b ? load_elem(b + col) : 0.f), f, df);
+            const float up = GATED ? acc[1].at(i, j) + (b ? load_elem(b + width + col) : 0.f) : 1.f;
+            const float qq = c.s.mlp ? q.at(i, j) : load_elem(dy + tok * o + col);
             part = fmaf(qq, f * up, part);
             da[row * c.s.first() + col] = g * qq * up * df;
             if (GATED) da[row * c.s.first() + width + col] = g * qq * f;

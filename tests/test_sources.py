@@ -23,3 +23,15 @@ def test_lanes_meet_before_they_overwrite_a_tiles_biases():
     read = text.index("reinterpret_cast<const float4 *>(gate_b", write)
     assert "__syncwarp()" in text[loop:write]
     assert "__syncwarp()" in text[write:read]
+
+
+def test_guarded_elements_are_read_by_ordinary_loads():
+    """`p < N ? load_elem(...) : 0` reads behind its test only if the load is
+    one the compiler may not move above it, which __ldg of 16-bit types is not."""
+    text = code("common.cuh")
+    assert "load_elem" in text and "__ldg" not in text
+    for name in sorted(os.listdir(CSRC)):
+        if name.endswith((".cu", ".cuh", ".h")):
+            # every __ldg left names a 32- or 128-bit array, none a generic element
+            for arg in re.findall(r"__ldg\(([^;]*)", code(name)):
+                assert not re.match(r"\(?(const )?(T|XT|__half|__nv_bfloat16)\b", arg), (name, arg)
