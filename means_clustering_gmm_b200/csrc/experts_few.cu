@@ -119,6 +119,10 @@ struct Lists {
     int segs;
 };
 
+// (what every kernel may use without a limit of its own)
+static_assert((kWarps + 1) * kExpFewPoints * 16 * sizeof(float) + sizeof(Lists) <= 48 * 1024,
+              "sums of the points and the lists");
+
 // One thread per pair.  A pair that repeats its point's expert has no entry of
 // its own; its weight goes to the first one's.
 __device__ __forceinline__ void make_lists(const ExpCall &c, Lists &L) {
@@ -459,9 +463,6 @@ template <typename T> cudaError_t launch_second(const ExpCall &c, cudaStream_t s
     int C = 8;
     while (C > 1 && tiles * C > 3 * 148) C /= 2;
     const size_t smem = (size_t)(kWarps + 1) * c.s.N * 16 * sizeof(float);
-    cudaError_t e = cudaFuncSetAttribute(few_second_kernel<T>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
     // starts under the first kernel's tail; its wait is for all of it
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -475,7 +476,7 @@ template <typename T> cudaError_t launch_second(const ExpCall &c, cudaStream_t s
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    e = cudaLaunchKernelEx(&cfg, few_second_kernel<T>, c, C);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, few_second_kernel<T>, c, C);
     if (e != cudaSuccess) return e;
     note_launches(1);
     return cudaGetLastError();

@@ -268,30 +268,33 @@ exp_scatter_kernel(ExpRoute rt) {
     }
 }
 
+// A kernel's limit of dynamic shared memory belongs to the function, not to a
+// launch: it is always set to what the largest call needs, so that calls of
+// other sizes on other threads cannot lower it between this and their launch.
+template <typename F> static cudaError_t allow_smem(F kernel, size_t bytes, size_t most) {
+    return bytes <= 40 * 1024 ? cudaSuccess
+                              : cudaFuncSetAttribute(kernel,
+                                                     cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                     (int)most);
+}
+
 cudaError_t launch_exp_route(const ExpCall &c, cudaStream_t s) {
     const ExpRoute &rt = c.rt;
     if (!rt.ids) return cudaSuccess;
     const int KK = rt.K + 1;
+    cudaError_t e;
     if (rt.P <= kOneBlockPairs && KK <= kOneBlockKeys) {
-        const int bytes = (35 * KK + 2) * (int)sizeof(int);
-        cudaError_t e = cudaSuccess;
-        if (bytes > 40 * 1024)
-            e = cudaFuncSetAttribute(exp_route_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     bytes);
+        const auto size = [](int keys) { return (35 * keys + 2) * sizeof(int); };
+        e = allow_smem(exp_route_kernel, size(KK), size(kOneBlockKeys));
         if (e != cudaSuccess) return e;
-        return exp_launch(exp_route_kernel, dim3(1), 1024, bytes, s, rt, c.err);
+        return exp_launch(exp_route_kernel, dim3(1), 1024, size(KK), s, rt, c.err);
     }
     const int64_t nch = (rt.P + rt.chunk - 1) / rt.chunk;
     const unsigned blocks = (unsigned)((nch + 3) / 4);
-    const int smem = 4 * KK * (int)sizeof(int);
-    cudaError_t e;
-    if (smem > 48 * 1024) {
-        e = cudaFuncSetAttribute(exp_hist_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
-        e = cudaFuncSetAttribute(exp_scatter_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 smem);
-        if (e != cudaSuccess) return e;
-    }
+    const size_t smem = 4 * KK * sizeof(int), most = 4 * (GMM_EXPERT_MAX_K + 1) * sizeof(int);
+    e = allow_smem(exp_hist_kernel, smem, most);
+    if (e == cudaSuccess) e = allow_smem(exp_scatter_kernel, smem, most);
+    if (e != cudaSuccess) return e;
     e = exp_launch(exp_hist_kernel, dim3(blocks), 128, smem, s, rt, c.err);
     if (e == cudaSuccess)
         e = exp_launch(exp_scan_kernel, dim3(KK), nch > 256 ? 1024 : 256, 0, s, rt, nch);

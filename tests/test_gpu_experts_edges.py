@@ -1,12 +1,16 @@
 """Calls of the experts' products that their documentation allows and whose
 faults depend on timing, on other calls or on unusual values, against the
 bounds of test_gpu_experts."""
+import ctypes
+import sys
+import threading
+
 import pytest
 import torch
 
-import means_clustering_gmm_b200 as gmm  # noqa: F401
+from means_clustering_gmm_b200 import _lib
 
-from .test_gpu_experts import check, inputs
+from .test_gpu_experts import check, forward, inputs, workspace
 
 pytestmark = pytest.mark.gpu
 
@@ -21,3 +25,57 @@ def test_biases_of_the_next_tile(h, gated):
     step = torch.arange(s["b1"].shape[1]) // 32 % 7
     s["b1"] = (s["b1"] + torch.arange(K)[:, None] - step).half()
     check(s, "silu", gated)
+
+
+def routed(seed, N, d, h, o, K, r, dtype="bf16"):
+    c = {k: t.cuda() if isinstance(t, torch.Tensor) else t
+         for k, t in inputs(seed, N, d, h, o, K, r, dtype).items()}
+    return c, workspace(c, False, False)
+
+
+@pytest.mark.parametrize("sizes", [
+    [dict(N=64, K=9, r=4), dict(N=1, K=9, r=4)],          # few points
+    [dict(N=100, K=300, r=2), dict(N=100, K=1000, r=2)],  # one-block routing
+    [dict(N=100, K=3100, r=2), dict(N=100, K=4096, r=2)],     # routing in steps
+])
+def test_threads_with_calls_of_different_sizes(sizes):
+    """Host threads, each with its stream and workspace, whose calls need
+    different amounts of shared memory of the same kernels."""
+    lib = _lib.load()
+    failed, results = [], []
+
+    def loop(c, ws, stream, y):
+        s = c["x"].shape + c["w2"].shape + c["ids"].shape
+        shape = _lib.ExpertShape(N=s[0], d=s[1], h=s[4], o=s[3], K=s[2], r=s[6],
+                                 dtype=_lib.GMM_BF16, activation=3, gated=0)
+        args = [ctypes.byref(shape)] + [
+            ctypes.c_void_p(c[k].data_ptr()) for k in ("x", "ids", "resp", "w1", "b1", "w2", "b2")]
+        args += [None, ctypes.c_void_p(y.data_ptr()), ctypes.c_void_p(ws.ptr), ws.nbytes, 0,
+                 ctypes.c_void_p(stream.cuda_stream)]
+        for i in range(10000):
+            status = lib.gmm_expert_mlp(*args)
+            if status:
+                failed.append(status)
+            if i % 100 == 99:
+                stream.synchronize()
+
+    threads = []
+    for i, kw in enumerate(2 * sizes):
+        c, ws = routed(50 + i, d=64, h=64, o=64, **kw)
+        want = forward(c, "silu", ws=ws)[0]
+        results.append((torch.empty_like(want), want))
+        args = (c, ws, torch.cuda.Stream(), results[-1][0])
+        threads.append(threading.Thread(target=loop, args=args))
+    torch.cuda.synchronize()
+    interval = sys.getswitchinterval()
+    sys.setswitchinterval(1e-6)
+    try:
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+    finally:
+        sys.setswitchinterval(interval)
+    torch.cuda.synchronize()
+    assert not failed, (len(failed), set(failed))
+    assert all(torch.equal(got, want) for got, want in results)
