@@ -286,8 +286,10 @@ static cudaError_t launch_simt_t(const T *X, int64_t N, int d, int K, const floa
     gmm_simt_lse_kernel<T><<<(unsigned)g1, 256, 0, s>>>(X, N, d, K, means, w.nhl, w.ck, w.lse,
                                                         loglik, w.ll_part, w.err);
     size_t smem = gmm_simt_stats_smem(d, p.tk, p.groups);
+    // (the limit is the function's: always the most a block may have, so that a
+    // call of another size on another thread cannot lower it before this launch)
     cudaError_t e = cudaFuncSetAttribute(gmm_simt_stats_kernel<T>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
     if (e != cudaSuccess) return e;
     dim3 grid(p.kchunks, p.ranges);
     gmm_simt_stats_kernel<T><<<grid, 256, smem, s>>>(X, N, d, K, p.tk, p.groups, p.range_pts,

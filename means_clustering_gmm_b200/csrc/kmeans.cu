@@ -474,10 +474,16 @@ static cudaError_t launch_kmeans_t(const T *X, int B, int64_t N, int d, int K, c
     else
         km_scan_kernel<int64_t><<<B, 1024, 0, s>>>(hist, N, K, L.nblk, segoff);
     size_t sc_smem = 8 * (size_t)K * sizeof(int32_t);
+    // (the limit is the function's: always the largest K's, so that a call of
+    // another K on another thread cannot lower it before this launch)
     cudaError_t e = cudaFuncSetAttribute(km_scatter_kernel,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sc_smem);
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         8 * KMEANS_MAX_K * (int)sizeof(int32_t));
     if (e != cudaSuccess) return e;
     km_scatter_kernel<<<g2, 256, sc_smem, s>>>(ids, N, K, L.nblk, hist, perm);
+    // (the sums read X through perm: never where it was not written)
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
     int64_t segs = (int64_t)B * K;
     double *segin = (double *)(ws + L.off_segin);
     const unsigned sgrid = (unsigned)((segs * 32 + 255) / 256);

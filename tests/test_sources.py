@@ -35,3 +35,13 @@ def test_guarded_elements_are_read_by_ordinary_loads():
             # every __ldg left names a 32- or 128-bit array, none a generic element
             for arg in re.findall(r"__ldg\(([^;]*)", code(name)):
                 assert not re.match(r"\(?(const )?(T|XT|__half|__nv_bfloat16)\b", arg), (name, arg)
+
+
+def test_shared_memory_limits_do_not_depend_on_the_call():
+    """A kernel's limit of dynamic shared memory is process-wide: set to one
+    call's own size it can be lowered by another thread before the launch."""
+    for name, own in (("kmeans.cu", "sc_smem"), ("gmm_simt.cu", "smem")):
+        calls = re.findall(r"cudaFuncSetAttribute\(([^;]*);", code(name))
+        assert calls
+        for c in calls:
+            assert not re.search(rf"\b{own}\b", c), (name, c)
