@@ -8,6 +8,8 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/gmm_b200.h"
 
 namespace gmmb {
@@ -89,6 +91,21 @@ inline GmmSimtPlan gmm_simt_plan(int64_t N, int d, int K) {
     p.lse_tiles = (N + kLseTileP - 1) / kLseTileP;
     return p;
 }
+
+// A property that launches ask for once per device (how many blocks are
+// resident, say): ask() gives the current device's, or 0 to be asked again.
+// Threads that ask at the same time store the same value.
+struct DeviceConstant {
+    static constexpr int kDevices = 64;
+    std::atomic<int> value[kDevices];
+    template <class F> int get(F ask) {
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || dev >= kDevices) return ask();
+        int v = value[dev].load(std::memory_order_relaxed);
+        if (v == 0) value[dev].store(v = ask(), std::memory_order_relaxed);
+        return v;
+    }
+};
 
 // Process-wide tracing state (abi.cu): launch counter and the optional
 // kernel timer events recorded around the dominant kernel of a call (the

@@ -769,13 +769,13 @@ cudaError_t launch_kind(const ExpCall &c, cudaStream_t st) {
     cfg.gridDim = dim3(kSms);
     int wave = kSms;
     if (CG == 2) {
-        static int resident = 0;
-        if (!resident) {
+        static DeviceConstant pairs;
+        const int resident = pairs.get([&] {
             int n = 0;
             e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
-            if (e != cudaSuccess) return e;
-            resident = n < 1 ? 2 : 2 * n;
-        }
+            return e != cudaSuccess ? 0 : n < 1 ? 2 : 2 * n;
+        });
+        if (e != cudaSuccess) return e;
         wave = resident < kSms ? resident : kSms;
     }
     const int64_t ctas = most * CG;

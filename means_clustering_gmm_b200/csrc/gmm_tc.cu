@@ -1226,14 +1226,13 @@ bool tc_shape_ok(gmm_dtype dt, int d, int K) {
 }
 
 int tc_sm_count() {
-    static int cached = 0;
-    if (!cached) {
-        int dev = 0;
+    static DeviceConstant sms;
+    return sms.get([] {
+        int dev = 0, n = 0;
         cudaGetDevice(&dev);
-        cudaDeviceGetAttribute(&cached, cudaDevAttrMultiProcessorCount, dev);
-        if (cached <= 0) cached = 148;
-    }
-    return cached;
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+        return n > 0 ? n : 148;
+    });
 }
 
 constexpr int kMaxRanges = 148;
@@ -1369,14 +1368,15 @@ static cudaError_t launch_direct(unsigned blocks, const XT *X, int64_t N, int d,
     auto kern = gmm_tc_direct_scores_kernel<XT>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kDirSmem);
     if (e != cudaSuccess) return e;
-    static int per_sm = 0;   // resident blocks per SM, asked once
-    if (per_sm == 0) {
+    static DeviceConstant resident;   // blocks per SM
+    const int per_sm = resident.get([&] {
         int nb = 0;
-        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&nb, kern, kDirThreads, kDirSmem) != cudaSuccess ||
-            nb < 1)
-            nb = 1;
-        per_sm = nb;
-    }
+        return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&nb, kern, kDirThreads, kDirSmem) !=
+                           cudaSuccess ||
+                       nb < 1
+                   ? 1
+                   : nb;
+    });
     const unsigned cap = (unsigned)(per_sm * tc_sm_count());
     if (blocks > cap) blocks = cap;
     kern<<<blocks, kDirThreads, kDirSmem, s>>>(X, N, d, means, vars, logw, dlist, dcount, dscore,
@@ -1419,16 +1419,16 @@ static cudaError_t launch_cluster(const XT *X, int64_t N, int K, const TcParams 
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    static int max_clusters = 0;   // per process: one device model
-    if (max_clusters <= 0) {
+    static DeviceConstant clusters;
+    const int max_clusters = clusters.get([&] {
         cfg.gridDim = dim3(kClu, kMaxRanges / kClu);
         int nc = 0;
         if (cudaOccupancyMaxActiveClusters(&nc, kern, &cfg) != cudaSuccess || nc < 1) {
             (void)cudaGetLastError();
             nc = tc_sm_count() / kClu;
         }
-        max_clusters = nc < kMaxRanges ? nc : kMaxRanges;
-    }
+        return nc < kMaxRanges ? nc : kMaxRanges;
+    });
     const int64_t ntiles = (N + kTileP - 1) / kTileP;
     int ranges = max_clusters;
     if (ranges > ntiles) ranges = (int)ntiles;

@@ -395,14 +395,13 @@ size_t km_tc_param_bytes(int B, int d, int K) {
 }
 
 static int kt_sm_count() {
-    static int cached = 0;
-    if (!cached) {
-        int dev = 0;
+    static DeviceConstant sms;
+    return sms.get([] {
+        int dev = 0, n = 0;
         cudaGetDevice(&dev);
-        cudaDeviceGetAttribute(&cached, cudaDevAttrMultiProcessorCount, dev);
-        if (cached <= 0) cached = 148;
-    }
-    return cached;
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+        return n > 0 ? n : 148;
+    });
 }
 
 template <int NB, typename XT>

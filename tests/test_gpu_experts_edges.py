@@ -2,6 +2,8 @@
 faults depend on timing, on other calls or on unusual values, against the
 bounds of test_gpu_experts."""
 import ctypes
+import os
+import subprocess
 import sys
 import threading
 
@@ -79,3 +81,37 @@ def test_threads_with_calls_of_different_sizes(sizes):
     torch.cuda.synchronize()
     assert not failed, (len(failed), set(failed))
     assert all(torch.equal(got, want) for got, want in results)
+
+
+FIRST_CALLS = """
+import threading, torch
+import means_clustering_gmm_b200 as gmm
+def call():
+    g = torch.Generator().manual_seed(1)
+    x = torch.randn(2000, 64, generator=g).bfloat16().cuda()
+    w = torch.randn(1, 128, 64, generator=g).bfloat16().cuda()
+    ws = gmm.Workspace.for_expert_linear(2000, 64, 128, 1, 0, x.dtype, backward=True)
+    barrier.wait()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        torch.cuda.current_stream().wait_stream(torch.cuda.default_stream())
+        y = gmm.expert_linear(x, None, None, w, None, ws, "silu")
+        got = gmm.expert_linear_backward(y, x, None, None, w, None, ws, "silu")[:2] + (y,)
+    torch.cuda.synchronize()
+    results.append(got)
+results, barrier = [], threading.Barrier(6)
+threads = [threading.Thread(target=call) for _ in range(6)]
+[t.start() for t in threads]
+[t.join() for t in threads]
+assert len(results) == 6
+assert all(torch.equal(a, b) for r in results for a, b in zip(r, results[0]))
+print("equal")
+"""
+
+
+def test_first_calls_on_several_threads():
+    """The first calls of a process, made at once: what the library asks the
+    device for once is asked by several threads."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    run = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True,
+                         text=True, timeout=120)
+    assert run.returncode == 0 and "equal" in run.stdout, run.stderr[-2000:]

@@ -45,3 +45,11 @@ def test_shared_memory_limits_do_not_depend_on_the_call():
         assert calls
         for c in calls:
             assert not re.search(rf"\b{own}\b", c), (name, c)
+
+
+def test_no_plain_static_is_written_by_the_calls():
+    """What launches ask a device for once is kept per device, in atomics."""
+    for name in sorted(os.listdir(CSRC)):
+        if name.endswith((".cu", ".cuh", ".h")):
+            assert not re.findall(r"^\s+static (?:int|unsigned|size_t|int64_t) \w+ = 0;", code(name),
+                                  re.M), name
