@@ -535,8 +535,12 @@ __global__ void __launch_bounds__(kThreads, 1) exp_tc_kernel(const __grid_consta
                 if (m < jn.valid && next_col < width) next_pair = rt.pair(jn.row0 + m);
             }
             __syncwarp();
+            // (a weight gradient's contraction is over its expert's points, of
+            // which there may be 2^31)
+            const long long limit =
+                kWaitLimitCycles + (C::kGrad ? j.steps1 * kStepLimitCycles : 0);
             if (!__all_sync(0xffffffffu, mbar_wait(&bars->accfull[buf], (tile >> 1) & 1, c.err,
-                                                   abort_flag)))
+                                                   abort_flag, limit)))
                 break;
             tc_fence_after();
             // column 0 of the (last phase's) accumulator, and q's

@@ -24,11 +24,13 @@
 namespace gmmb {
 namespace tc {
 
-// Upper bound of any wait in these kernels, in SM clock cycles (~2 s): every
-// wait is on a producer inside the same CTA, so it ends in microseconds
-// unless something is wrong; then the kernel records GMM_ERR_TIMEOUT and
-// unwinds instead of hanging.
+// Upper bound of a wait, in SM clock cycles (~2 s): what is waited for (a copy,
+// a product, the other warps or CTAs of a cluster) takes microseconds unless
+// something is wrong; then the kernel records GMM_ERR_TIMEOUT and unwinds
+// instead of hanging.  A wait for a whole contraction adds kStepLimitCycles for
+// each of its steps, which take 250 to 1000.
 constexpr long long kWaitLimitCycles = 4000000000LL;
+constexpr long long kStepLimitCycles = 8192;
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) {
     return (uint32_t)__cvta_generic_to_shared(p);
@@ -67,13 +69,14 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t *bar, uint32_t parity) {
 // records GMM_ERR_TIMEOUT, and raises the CTA's abort flag) if the limit
 // ran out or another thread of the CTA already aborted.
 __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, int *err,
-                                          volatile int *abort_flag) {
+                                          volatile int *abort_flag,
+                                          long long limit = kWaitLimitCycles) {
     if (mbar_try_wait(bar, parity)) return true;
     long long t0 = clock64();
     while (true) {
         if (mbar_try_wait(bar, parity)) return true;
         if (*abort_flag) return false;
-        if (clock64() - t0 > kWaitLimitCycles) {
+        if (clock64() - t0 > limit) {
             set_error(err, GMM_ERR_TIMEOUT);
             *abort_flag = 1;
             return false;

@@ -10,6 +10,7 @@ import threading
 import pytest
 import torch
 
+import means_clustering_gmm_b200 as gmm
 from means_clustering_gmm_b200 import _lib
 
 from .test_gpu_experts import check, forward, inputs, workspace
@@ -115,3 +116,21 @@ def test_first_calls_on_several_threads():
     run = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True,
                          text=True, timeout=120)
     assert run.returncode == 0 and "equal" in run.stdout, run.stderr[-2000:]
+
+
+def test_gradient_over_a_billion_points():
+    """A weight gradient whose contraction, one tile's, takes longer than the
+    limit of an ordinary wait."""
+    N, d, o = 1_400_000_000, 8, 8
+    rows = [0, 63, 64, N // 2, 2 ** 30 + 1, N - 65, N - 1]
+    g = torch.Generator().manual_seed(61)
+    some = torch.randint(-3, 4, (2, len(rows), d), generator=g).bfloat16()
+    x = torch.zeros(N, d, dtype=torch.bfloat16, device="cuda")
+    dy = torch.zeros(N, o, dtype=torch.bfloat16, device="cuda")
+    x[rows], dy[rows] = some[0].cuda(), some[1].cuda()
+    w = torch.eye(8, dtype=torch.bfloat16, device="cuda")[None]
+    ws = gmm.Workspace.for_expert_linear(N, d, o, 1, 0, x.dtype, backward=True)
+    dX, dW, _, _ = gmm.expert_linear_backward(dy, x, None, None, w, None, ws)
+    assert gmm.gmm_last_error(ws) == 0
+    assert torch.equal(dW[0].cpu().float(), some[1].float().T @ some[0].float())
+    assert torch.equal(dX[rows].cpu(), some[1]) and not dX[1:63].any()
