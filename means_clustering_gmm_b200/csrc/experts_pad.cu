@@ -2,9 +2,10 @@
 //
 // The tensor-core kernels read rows of whole 16-byte units.  With every width
 // rounded up and zeros in the new rows and columns the padded problem has the
-// same results in the old ones: a padded hidden unit has pre-activation
-// f(0) = 0 (times 0), padded columns of W2 give it the gradient 0, and padded
-// contraction indices add products of zeros.  Only experts in use are copied.
+// same results in the old ones: padded contraction indices add products of
+// zeros on both sides, and what a hidden unit that does not exist would get
+// (0 times an infinity of the point is not 0) is set to 0 by the epilogue that
+// forms it.  Only experts in use are copied.
 // Bound by the copies: about three passes over the used weights, where the
 // CUDA-core form of such a call multiplies 64-row tiles for a few points.
 #include "experts.h"

@@ -607,6 +607,17 @@ __global__ void __launch_bounds__(kThreads, 1) exp_tc_kernel(const __grid_consta
                         up[2 * i + 1] = __fadd2_rn(pair_of(r1, 2 * i + 1), make_float2(b.z, b.w));
                     }
                 }
+                if constexpr (KIND == kFirst || KIND == kDaMlp)
+                    if (s.mlp && col + 16 > c.units)   // padded copies, or the last columns
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (col + i >= c.units) {
+                                if (i & 1) x[i / 2].y = 0.f; else x[i / 2].x = 0.f;
+                                if constexpr (GATED) {
+                                    if (i & 1) up[i / 2].y = 0.f; else up[i / 2].x = 0.f;
+                                }
+                                if constexpr (C::kTwo) r2[i] = 0u;
+                            }
                 if constexpr (C::kGrad) {
                     const int M = KIND == kDw2 ? s.o : s.first();
                     T *out = (T *)(KIND == kDw2 ? c.dw2 : c.dw1);

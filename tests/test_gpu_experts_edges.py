@@ -13,7 +13,7 @@ import torch
 import means_clustering_gmm_b200 as gmm
 from means_clustering_gmm_b200 import _lib
 
-from .test_gpu_experts import check, forward, inputs, workspace
+from .test_gpu_experts import backward, check, cuda, forward, inputs, workspace
 
 pytestmark = pytest.mark.gpu
 
@@ -134,3 +134,27 @@ def test_gradient_over_a_billion_points():
     assert gmm.gmm_last_error(ws) == 0
     assert torch.equal(dW[0].cpu().float(), some[1].float().T @ some[0].float())
     assert torch.equal(dX[rows].cpu(), some[1]) and not dX[1:63].any()
+
+
+@pytest.mark.parametrize("flags", [0, gmm.GMM_FLAG_FORCE_SIMT])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("N,d,h,o,r", [(40, 7, 5, 3, 2), (70, 8, 13, 8, 1), (900, 50, 61, 70, 1),
+                                       (90, 64, 72, 64, 2)])
+def test_an_infinity_behind_relu(N, d, h, o, r, dtype, flags):
+    """Hidden units at minus infinity are 0 behind relu, and so is their
+    gradient: a point with an infinite coordinate has the results of one with a
+    large coordinate, whatever copies the widths need.  Only dW1 of its experts
+    holds 0 * inf, in that coordinate's column."""
+    s = inputs(71, N, d, h, o, 3, r, dtype)
+    s["w1"][:, :, 2] = -s["w1"][:, :, 2].abs() - 1
+    big = dict(s, x=s["x"].clone())
+    big["x"][5, 2] = 2.0 ** 14
+    inf = dict(s, x=s["x"].clone())
+    inf["x"][5, 2] = float("inf")
+    y, want = (forward(cuda(t), "relu", flags=flags)[0] for t in (inf, big))
+    assert want.isfinite().all() and torch.equal(y, want)
+    got, want = (backward(cuda(t), "relu", flags=flags)[0] for t in (inf, big))
+    for t in (got, want):
+        t["dw1"][s["ids"][5].long(), :, 2] = 0
+    for k in want:
+        assert want[k].isfinite().all() and torch.equal(got[k], want[k]), k
