@@ -2,6 +2,8 @@
 // checks, workspace layout and the order of the launches.
 #include "experts.h"
 
+#include <climits>
+
 using namespace gmmb;
 
 namespace {
@@ -276,7 +278,7 @@ gmm_status forward(const gmm_expert_shape *shape, bool mlp, const void *X, const
     k.workspace(ws, ws_bytes, total_bytes(p, false, flags));
     if (!k.ok) return GMM_ERR_INVALID_ARG;
     ExpCall c = make_call(q, L, ws, ids);
-    c.units = p.h;
+    c.units = mlp ? p.h : INT_MAX;
     c.x = X;
     c.w1 = W1;
     c.b1 = b1;
@@ -322,7 +324,7 @@ gmm_status backward(const gmm_expert_shape *shape, bool mlp, const void *dY, con
     k.workspace(ws, ws_bytes, total_bytes(p, true, flags));
     if (!k.ok) return GMM_ERR_INVALID_ARG;
     ExpCall c = make_call(q, L, ws, ids);
-    c.units = p.h;
+    c.units = mlp ? p.h : INT_MAX;
     c.dy = dY;
     c.x = X;
     c.w1 = W1;

@@ -103,7 +103,7 @@ struct ExpCall {
     int64_t max_rows;
     int nrpart;         // partial sums of dresp per pair
     size_t esize;       // bytes per element of hid and da
-    int units;          // hidden units that exist; padded copies have more
+    int units;          // hidden units that exist (padded copies have more); linear: no limit
 };
 
 // The activation and its derivative.

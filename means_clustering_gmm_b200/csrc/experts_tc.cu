@@ -73,6 +73,7 @@ enum Kind {
 template <int KIND, bool GATED, int CG, int W> struct Cfg {
     static constexpr bool kGrad = KIND == kDw1 || KIND == kDw2;
     static constexpr bool kTwo = KIND == kDaMlp;
+    static constexpr bool kHidden = KIND == kFirst || KIND == kDaMlp;   // columns: hidden units
     static constexpr int NB = kTwo ? 128 : GATED ? W / 2 : W;
     static constexpr int N1 = kTwo ? 128 : W;
     static constexpr int N2 = kTwo ? (GATED ? 256 : 128) : 0;
@@ -585,9 +586,18 @@ __global__ void __launch_bounds__(kThreads, 1) exp_tc_kernel(const __grid_consta
                 float2 x[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) x[i] = pair_of(r0, i);
-                if (!has)
+                // columns of this group that have a value (padded copies end
+                // with hidden units that do not exist)
+                const int live = !has ? 0 : C::kHidden ? c.units - col : 16;
+                if (live < 16)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] = splat(0.f);
+                    for (int i = 0; i < 16; ++i)
+                        if (i >= live) {
+                            if (i & 1) x[i / 2].y = 0.f;
+                            else x[i / 2].x = 0.f;
+                            if constexpr (GATED) r1[i] = 0u;
+                            if constexpr (C::kTwo) r2[i] = 0u;
+                        }
                 if constexpr (C::kBias) {
                     const float4 *gb = reinterpret_cast<const float4 *>(gate_b + c0 - pt * kPart);
 #pragma unroll
@@ -607,17 +617,6 @@ __global__ void __launch_bounds__(kThreads, 1) exp_tc_kernel(const __grid_consta
                         up[2 * i + 1] = __fadd2_rn(pair_of(r1, 2 * i + 1), make_float2(b.z, b.w));
                     }
                 }
-                if constexpr (KIND == kFirst || KIND == kDaMlp)
-                    if (s.mlp && col + 16 > c.units)   // padded copies, or the last columns
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (col + i >= c.units) {
-                                if (i & 1) x[i / 2].y = 0.f; else x[i / 2].x = 0.f;
-                                if constexpr (GATED) {
-                                    if (i & 1) up[i / 2].y = 0.f; else up[i / 2].x = 0.f;
-                                }
-                                if constexpr (C::kTwo) r2[i] = 0u;
-                            }
                 if constexpr (C::kGrad) {
                     const int M = KIND == kDw2 ? s.o : s.first();
                     T *out = (T *)(KIND == kDw2 ? c.dw2 : c.dw1);
