@@ -28,6 +28,14 @@ def _stream_ptr(stream) -> int:
     return int(stream.cuda_stream)
 
 
+def keep_for(stream, *tensors) -> None:
+    """The tensors' memory is not handed out again before what `stream` holds
+    now is done (nothing to do for tensors that belong to it)."""
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 

@@ -15,9 +15,11 @@ Argument marshalling only, as in ``api``; include/gmm_b200.h states each
 operation.  Calls that share a workspace must not overlap in time on the
 device (two captured graphs that may run at once need one each).  ``stream``
 (default: the current one of X's device) is where a call runs and its outputs
-belong; its inputs have to be ready there.  Bases of X, dY, the weights and
-``out`` must be 16-byte aligned (whole tensors are).  An id at or
-above K is skipped and recorded: ``gmm_last_error(ws)`` reports GMM_ERR_RANGE.
+belong; its inputs have to be ready there.  Arrays given to a call with
+``stream`` may be dropped at once: their memory is kept until it is done.
+Bases of X, dY, the weights and ``out`` must be 16-byte aligned (whole tensors
+are).  An id at or above K is skipped and recorded: ``gmm_last_error(ws)``
+reports GMM_ERR_RANGE.
 """
 from __future__ import annotations
 
@@ -27,7 +29,7 @@ import torch
 
 from . import _lib
 from ._lib import GMM_FLAG_NONE, ExpertShape, check
-from .api import _DT, Workspace
+from .api import _DT, Workspace, keep_for
 
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3}
 
@@ -92,7 +94,7 @@ class _Call:
     not, so that outputs belong to the stream that writes them."""
 
     __slots__ = ("dev", "dtype", "N", "d", "h", "o", "K", "r", "first", "shape", "ws", "stream",
-                 "guard")
+                 "guard", "side")
 
     def __init__(self, X, ids, resp, W1, W2, ws, activation, gated, stream):
         if not isinstance(X, torch.Tensor) or X.dim() != 2 or X.dtype not in _DT or not X.is_cuda:
@@ -133,7 +135,7 @@ class _Call:
         self.dev, self.dtype, self.ws = dev, dtype, ws
         self.N, self.d, self.h, self.o, self.K, self.r, self.first = N, d, h, o, K, r, first
         self.shape = _shape(N, d, h, o, K, r, dtype, activation, bool(gated))
-        self.guard = None
+        self.guard, self.side = None, stream
         if stream is not None:
             if stream.device != dev:
                 raise ValueError(f"stream is on {stream.device}, X on {dev}")
@@ -165,6 +167,8 @@ class _Call:
     def run(self, name, fn, flags, *args):
         check(name, fn(self.shape, *[None if t is None else t.data_ptr() for t in args],
                        self.ws.ptr, self.ws.nbytes, int(flags), self.stream))
+        if self.side is not None:
+            keep_for(self.side, self.ws.buf, *args)
 
 
 def _like(t):

@@ -158,3 +158,35 @@ def test_an_infinity_behind_relu(N, d, h, o, r, dtype, flags):
         t["dw1"][s["ids"][5].long(), :, 2] = 0
     for k in want:
         assert want[k].isfinite().all() and torch.equal(got[k], want[k]), k
+
+
+@pytest.mark.parametrize("h", [0, 72])
+def test_arrays_may_be_dropped_after_a_call_on_a_stream(h):
+    """What a call with ``stream`` still has to read is not handed out again:
+    the stream is kept busy, everything dropped, and new arrays of the same
+    sizes get other memory."""
+    c = cuda(inputs(81, 300, 64, h, 64, 3, 2, "bf16", res=True))
+    want, want_g = forward(c, "silu")[0], backward(c, "silu")[0]
+    side = torch.cuda.Stream()
+    for call, keep in ((forward, ("w1", "w2", "b1", "b2", "x", "ids", "resp", "res")),
+                       (backward, ("w1", "w2", "b1", "b2", "x", "ids", "resp", "dy"))):
+        call(c, "silu", stream=side)   # (the stream's own memory)
+        s = {k: t.clone() if isinstance(t, torch.Tensor) else t for k, t in c.items()}
+        ws = workspace(s, False, call is backward)
+        torch.cuda.synchronize()
+        busy = {t.data_ptr(): (t.shape, t.dtype) for t in
+                [s[k] for k in keep if s[k] is not None] + [ws.buf]}
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(1_000_000_000)   # clocks: 0.5 s
+        got = call(s, "silu", ws=ws, stream=side)[0]
+        del s, ws
+        new = [torch.empty(v[0], dtype=v[1], device="cuda") for v in busy.values()]
+        assert not side.query()   # (otherwise nothing is shown)
+        assert not busy.keys() & {t.data_ptr() for t in new}
+        for t in new:
+            t.fill_(1)
+        torch.cuda.synchronize()
+        if call is forward:
+            assert torch.equal(got, want)
+        else:
+            assert all(torch.equal(got[k], want_g[k]) for k in want_g)
