@@ -2,7 +2,9 @@
 
 Argument marshalling only: every step of the computation runs in the CUDA
 kernels of libgmm_b200.so.  PyTorch provides the device memory (outputs and
-workspaces) and the stream (``torch.cuda.current_stream()`` by default).
+workspaces) and the stream (``torch.cuda.current_stream()`` by default).  A
+call with ``stream`` expects its inputs to be ready there; arrays may be dropped
+while it runs.
 """
 from __future__ import annotations
 
@@ -34,6 +36,19 @@ def keep_for(stream, *tensors) -> None:
     for t in tensors:
         if t is not None:
             t.record_stream(stream)
+
+
+def _on(stream, call, *args, **kw):
+    """call(*args, **kw) with `stream` current, so that what it allocates and
+    prepares is that stream's.  The memory of what is given is kept until the
+    stream has used it, that of what is returned until the caller's stream has."""
+    here = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        out = call(*args, **kw)
+    tensors = [a.buf if isinstance(a, Workspace) else a for a in (*args, *kw.values())]
+    keep_for(stream, *(t for t in tensors if isinstance(t, torch.Tensor) and t.is_cuda))
+    keep_for(here, *(t for t in out if isinstance(t, torch.Tensor) and t.is_cuda))
+    return out
 
 
 def _ptr(t):
@@ -142,6 +157,9 @@ def gmm_em_step(X: torch.Tensor, means: torch.Tensor, variances: torch.Tensor,
                 want_loglik: bool = False, flags: int = GMM_FLAG_NONE, stream=None):
     """Fused E-step + statistics.  Returns (stats [K, 1+2d] fp64 laid out as
     S0|S1|S2 in memory, loglik [N] fp32 or None, loglik_total [1] fp64)."""
+    if stream is not None:
+        return _on(stream, gmm_em_step, X, means, variances, logw, ws, stats, loglik, loglik_total,
+                   want_loglik, flags)
     N, d = X.shape
     K = means.shape[0]
     if X.dtype not in _DT or not X.is_cuda or not X.is_contiguous():
@@ -167,6 +185,8 @@ def gmm_em_step(X: torch.Tensor, means: torch.Tensor, variances: torch.Tensor,
 def gmm_finalize(stats: torch.Tensor, N: int, means: torch.Tensor, variances: torch.Tensor,
                  logw: torch.Tensor, ws: Workspace, var_floor: float = 1e-6, stream=None):
     """M-step finalise; updates means/variances/logw in place."""
+    if stream is not None:
+        return _on(stream, gmm_finalize, stats, N, means, variances, logw, ws, var_floor)
     K, d = means.shape
     rc = _lib.load().gmm_finalize(stats.data_ptr(), N, d, K, float(var_floor), means.data_ptr(),
                                   variances.data_ptr(), logw.data_ptr(), ws.ptr, ws.nbytes,
@@ -196,6 +216,8 @@ def soft_assign(X: torch.Tensor, means: torch.Tensor, variances: torch.Tensor,
     """Top-r components per point with responsibility >= tau (gmm_soft_assign).
     Returns (ids [N, r] int32 with -1 past the cut, resp [N, r] fp32, loglik
     [N] or None)."""
+    if stream is not None:
+        return _on(stream, soft_assign, X, means, variances, logw, r, tau, ws, want_loglik, flags)
     N, d = X.shape
     K = means.shape[0]
     if X.dtype not in _DT or not X.is_cuda or not X.is_contiguous():
@@ -240,6 +262,8 @@ def gmm_em_step_batched(X: torch.Tensor, means: torch.Tensor, variances: torch.T
     """Fused E-step + statistics of B independent problems: X [B, N, d],
     means/variances [B, K, d], logw [B, K].  Returns (stats [B, K*(1+2d)]
     fp64, loglik [B, N] or None, loglik_total [B] fp64)."""
+    if stream is not None:
+        return _on(stream, gmm_em_step_batched, X, means, variances, logw, ws, want_loglik, flags)
     B, N, d = X.shape
     K = means.shape[1]
     if X.dtype not in _DT or not X.is_cuda or not X.is_contiguous():
@@ -263,6 +287,8 @@ def gmm_finalize_batched(stats: torch.Tensor, N: int, means: torch.Tensor,
                          variances: torch.Tensor, logw: torch.Tensor, ws: Workspace,
                          var_floor: float = 1e-6, stream=None):
     """M-step finalise of B problems in place (one launch)."""
+    if stream is not None:
+        return _on(stream, gmm_finalize_batched, stats, N, means, variances, logw, ws, var_floor)
     B, K, d = means.shape
     rc = _lib.load().gmm_finalize_batched(stats.data_ptr(), B, N, d, K, float(var_floor),
                                           means.data_ptr(), variances.data_ptr(), logw.data_ptr(),
@@ -282,6 +308,8 @@ def fit(X, means, variances, logw, max_iters: int = 100, tol: float = 1e-6, ws=N
     tensors are copied to the device first and the fitted parameters are
     copied back.  Returns (means, vars, logw, loglik_trace [iterations run]
     fp64, converged: bool)."""
+    if stream is not None:
+        return _on(stream, fit, X, means, variances, logw, max_iters, tol, ws, var_floor, flags)
     host = not X.is_cuda
     dev = torch.device("cuda")
     Xd = X.to(dev, non_blocking=True) if host else X
@@ -323,6 +351,8 @@ def init_kmeans(X: torch.Tensor, centroids: torch.Tensor, iters: int = 10, var_f
     """GMM start from k-means (gmm_init_kmeans): `iters` Lloyd iterations
     from `centroids` [K, d], then the hard partition's M-step.  Returns
     (means, vars, logw[, ids]) on the device."""
+    if stream is not None:
+        return _on(stream, init_kmeans, X, centroids, iters, var_floor, ws, want_ids)
     N, d = X.shape
     K = centroids.shape[0]
     if X.dtype not in _DT or not X.is_cuda or not X.is_contiguous():
@@ -349,6 +379,9 @@ def kmeans_step(X: torch.Tensor, centroids: torch.Tensor, ws: Workspace,
     """One Lloyd iteration for B problems: X [B, N, d] (or [N, d]), centroids
     [B, K, d] fp32.  Returns (ids [B, N] int32, new_centroids, counts [B, K]
     int32, inertia [B] fp64)."""
+    if stream is not None:
+        return _on(stream, kmeans_step, X, centroids, ws, ids, new_centroids, counts, inertia,
+                   flags)
     squeeze = X.dim() == 2
     if squeeze:
         X = X.unsqueeze(0)
