@@ -51,6 +51,8 @@ def _shape(N, d, h, o, K, r, dtype, activation="none", gated=False):
             raise ValueError("dtype must be float32, bfloat16 or float16")
         if len(_shapes) >= 4096:
             _shapes.clear()
+        # (ctypes would cut larger numbers down to valid ones)
+        N, d, h, o, K, r = (v if abs(v) < 1 << 31 else -1 for v in (N, d, h, o, K, r))
         p = _shapes[key] = ctypes.pointer(ExpertShape(
             N=N, d=d, h=h, o=o, K=K, r=r, dtype=_DT[dtype], activation=ACTIVATIONS[activation],
             gated=int(bool(gated))))
