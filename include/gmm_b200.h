@@ -414,8 +414,16 @@ gmm_status kmeans_step(const void *X, gmm_dtype dtype, int B, int64_t N, int d, 
  * contractions over 2048, where FMA is within 7e-7).  Results are rounded to
  * `dtype` once; for 16-bit types the hidden vector h and, in the backward
  * pass, the gradients of the pre-activations and g h are rounded to `dtype`
- * as well, because they are operands of the next tensor-core product.  Every
- * sum has a fixed order: results are bitwise reproducible.
+ * as well, because they are operands of the next tensor-core product: a
+ * gradient is off by about 1.4 times the error of its own rounding.  Nothing
+ * scales them: float16 gradients of the pre-activations below 6e-5 lose bits
+ * as subnormals do, so scale dY where they are small.  Every sum has a fixed
+ * order: results are bitwise reproducible.
+ *
+ * The activations of 16-bit calls use hardware exponentials and reciprocals
+ * (silu within 2^-20 + 2^-23 |z| of itself) and, for gelu, erfc by Abramowitz and Stegun 7.1.26:
+ * Phi within 2^-23, which is 5e-4 of gelu at -4, 4e-3 at -6 and 2e-2 at -10,
+ * where gelu is 1e-4, 6e-9 and 8e-23.  fp32 calls use erfcf and expf.
  *
  * The kernels, by sizes and types (gmm_expert_path):
  *   2  16-bit types: grouped products on the tensor cores (tcgen05); where d,
@@ -459,6 +467,13 @@ int gmm_expert_path(const gmm_expert_shape *shape, int backward, uint32_t flags)
  * (backward = 1) call of this shape needs with these flags (0 for an invalid
  * shape).  A workspace of the backward call serves the forward call too.
  * Clear its error word once with gmm_workspace_init.
+ *
+ * It grows with N r without a bound: 4 bytes for each of N r entries and the
+ * o (backward: d) columns of a result where r > 1, and the rows that the
+ * products hand on: for 16-bit types 2 (d + h) bytes an entry forward, 2 (d +
+ * o + h + rows of W1) backward; fp32 4 h forward, 4 (h + rows of W1) backward
+ * (of the linear form no h, and backward no o).  10 million points with r = 8 and
+ * o = 128 take 41 GB for the first alone: call with fewer points at a time.
  */
 size_t gmm_expert_workspace_size(const gmm_expert_shape *shape, int backward, uint32_t flags);
 
@@ -471,8 +486,9 @@ size_t gmm_expert_workspace_size(const gmm_expert_shape *shape, int backward, ui
  *   flags    0, or GMM_FLAG_FORCE_SIMT (CUDA-core kernels).
  * Errors: GMM_ERR_INVALID_ARG for NULL or misaligned pointers (X, weights,
  * Y, dY and the gradients of X and the weights 16 bytes, the workspace 256,
- * the others their element), invalid shapes and flags, a short workspace;
- * GMM_ERR_CUDA if a launch fails.  Nothing is launched then.
+ * the others their element), invalid shapes and flags, a short workspace:
+ * nothing is launched then.  GMM_ERR_CUDA if a launch fails: those before it
+ * in the call still run, and what the call writes is undefined.
  */
 gmm_status gmm_expert_linear(const gmm_expert_shape *shape, const void *X, const int32_t *ids,
                              const float *resp, const void *W, const void *b,

@@ -13,7 +13,8 @@ import torch
 import means_clustering_gmm_b200 as gmm
 from means_clustering_gmm_b200 import _lib
 
-from .test_gpu_experts import backward, check, cuda, forward, inputs, workspace
+from .test_gpu_experts import (DT, act, backward, check, cuda, dact, forward, half_step, inputs, tiny,
+                               workspace)
 
 pytestmark = pytest.mark.gpu
 
@@ -190,3 +191,39 @@ def test_arrays_may_be_dropped_after_a_call_on_a_stream(h):
             assert torch.equal(got, want)
         else:
             assert all(torch.equal(got[k], want_g[k]) for k in want_g)
+
+
+@pytest.mark.parametrize("N", [64, 1600])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("activation", ["gelu", "silu"])
+def test_activations_of_16_bit_calls(activation, dtype, N):
+    """f and f' at known arguments (identity weights), as include/gmm_b200.h
+    bounds them.  gelu: 2^-23 of |z| from the distribution function (its
+    formula's 7.5e-8 is 2^-23.7, its fp32 sums the rest), and the exponential's
+    2^-20 (1 + z^2) relative to the tail.  silu: relative to f, 2^-20 + |z| 2^-23.
+    Results are rounded once, the gradient twice (da is rounded too)."""
+    dt, n8 = DT[dtype], N * 8
+    z = torch.cat([torch.linspace(-14, 14, n8 - 8), torch.tensor([0.0, -0.0, 60, -60, 80, -80, 200,
+                                                                  -200])]).to(dt).view(N, 8)
+    one = torch.ones(N, 8, dtype=dt)
+    w = torch.eye(8, dtype=dt)[None].cuda()
+    ws = gmm.Workspace.for_expert_linear(N, 8, 8, 1, 0, dt, backward=True)
+    y = gmm.expert_linear(z.cuda(), None, None, w, None, ws, activation).cpu().double()
+    dx = gmm.expert_linear_backward(one.cuda(), z.cuda(), None, None, w, None, ws,
+                                    activation)[0].cpu().double()
+    z = z.double()
+    f, df = act(z, activation), dact(z, activation)
+    if activation == "gelu":
+        tail = 0.5 * torch.erfc(z.abs() / 2 ** 0.5)
+        cdf = 2.0 ** -23 + 2.0 ** -20 * (1 + z * z) * tail
+        ef = z.abs() * cdf
+        edf = cdf + (2.0 ** -20 + 2.0 ** -22 * z * z) * z.abs() * torch.exp(-z * z / 2)
+    else:
+        rel = 2.0 ** -20 + 2.0 ** -23 * z.abs()
+        p = torch.sigmoid(z)
+        ef = rel * f.abs() + 2.0 ** -126 * z.abs()
+        edf = rel * (p + 2 * f.abs()) + 2.0 ** -126 * (1 + z.abs())
+    u = half_step(dt)
+    assert ((y - f).abs() <= ef + u * (f.abs() + ef) + tiny(dt)).all()
+    err = (dx - df).abs() - (edf + 2 * u * (1 + u) * (df.abs() + edf) + 2 * tiny(dt))
+    assert (err <= 0).all(), (err.max(), z.flatten()[err.argmax()])
