@@ -227,3 +227,56 @@ def test_activations_of_16_bit_calls(activation, dtype, N):
     assert ((y - f).abs() <= ef + u * (f.abs() + ef) + tiny(dt)).all()
     err = (dx - df).abs() - (edf + 2 * u * (1 + u) * (df.abs() + edf) + 2 * tiny(dt))
     assert (err <= 0).all(), (err.max(), z.flatten()[err.argmax()])
+
+
+@pytest.mark.parametrize("N,d,o,dtype", [(3, 64, 72, "bf16"), (300, 64, 72, "f16"),
+                                         (300, 33, 21, "bf16"), (40, 64, 24, "f32")])
+def test_a_captured_fork_and_join(N, d, o, dtype):
+    """Inside one graph: inputs written on one stream just before calls on it
+    and on another one, a workspace each, both joined and their results added;
+    replayed with new contents."""
+    c = cuda(inputs(91, N, d, 48, o, 5, 2, dtype, res=True, cut=0.2))
+    spaces = [workspace(c, False, True) for _ in range(2)]
+    fresh = {k: c[k].clone() for k in ("x", "dy", "resp", "ids")}
+    side = torch.cuda.Stream()
+
+    def step():
+        here = torch.cuda.current_stream()
+        for k, t in fresh.items():
+            c[k].copy_(t)
+        side.wait_stream(here)
+        y = forward(c, "silu", ws=spaces[0])[0]
+        with torch.cuda.stream(side):
+            g = backward(c, "silu", ws=spaces[1])[0]
+            g["dx"].mul_(2)
+        here.wait_stream(side)
+        return forward(dict(c, res=y), "silu", ws=spaces[1])[0], g
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y, g = step()
+    for turn in range(3):
+        fresh["x"].copy_(torch.randn(N, d, device="cuda"))
+        fresh["ids"].copy_(torch.randint(-1, 5, (N, 2), device="cuda"))
+        graph.replay()
+        torch.cuda.synchronize()
+        want_y, want_g = step()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want_y) and all(torch.equal(g[k], want_g[k]) for k in want_g)
+
+
+@pytest.mark.parametrize("N,r,h", [(5, 2, 0), (300, 1, 0), (300, 2, 31), (300, 0, 31), (900, 1, 30)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_result_may_replace_the_residual_at_odd_widths(N, r, h, dtype):
+    c = cuda(inputs(92, N, 33, h, 21, 3 if r else 1, r, dtype, res=True))
+    want = forward(c, "silu")[0]
+    assert torch.equal(forward(c, "silu", out=c["res"])[0], want)
+
+
+@pytest.mark.parametrize("K,N,r", [(4096, 700, 8), (4096, 20, 8), (1023, 2000, 2), (1024, 500, 1)])
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
+def test_many_experts(K, N, r, dtype):
+    """The most experts, and both sides of the one-block routing's limit."""
+    check(inputs(93, N, 16, 0, 8, K, r, dtype, cut=0.1), "silu")
