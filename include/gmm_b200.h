@@ -410,8 +410,9 @@ gmm_status kmeans_step(const void *X, gmm_dtype dtype, int B, int64_t N, int d, 
  * a dense layer, f(X W^T + b) + residual.
  *
  * Sums are fp32 (FMA, or tensor-core accumulators, which truncate: dresp, the
- * one fp32 result of a 16-bit call, is within 6e-6 of its 2-norm after
- * contractions over 2048, where FMA is within 7e-7).  Results are rounded to
+ * one fp32 result of a 16-bit call, loses 1e-9 of its 2-norm with each index of
+ * its contractions: 2e-6 of the linear form's after 2048 and 4e-6 to 6e-6 of the
+ * gated layer's, where FMA is within 7e-7).  Results are rounded to
  * `dtype` once; for 16-bit types the hidden vector h and, in the backward
  * pass, the gradients of the pre-activations and g h are rounded to `dtype`
  * as well, because they are operands of the next tensor-core product: a
@@ -430,8 +431,9 @@ gmm_status kmeans_step(const void *X, gmm_dtype dtype, int B, int64_t N, int d, 
  *      h or o is not a multiple of 8, on zero-padded copies in the workspace;
  *   1  16-bit types, d, h and o multiples of 8, at most 64 points and
  *      GMM_EXPERT_FEW_PAIRS pairs, forward only: kernels that stream each used
- *      expert's weights once;
- *   0  fp32, and GMM_FLAG_FORCE_SIMT: CUDA cores.
+ *      expert's weights once for every 32 of its points;
+ *   0  fp32, and GMM_FLAG_FORCE_SIMT: CUDA cores.  With the flag, calls of
+ *      16-bit types too keep every sum and intermediate array in fp32.
  */
 typedef enum gmm_activation {
     GMM_ACT_NONE = 0,

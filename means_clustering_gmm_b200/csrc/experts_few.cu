@@ -1,6 +1,7 @@
 // The experts' products for few points (16-bit types, widths multiples of 8,
 // at most kExpFewPoints points and GMM_EXPERT_FEW_PAIRS pairs): each used
-// expert's weights are read once, and that read is the bound.
+// expert's weights are read once for every 32 of its points, and that read is
+// the bound.
 //
 //   few_first_kernel   a block is 16 or 32 rows of one expert's first weight;
 //                      the blocks of a pair whose expert an earlier pair

@@ -1,5 +1,4 @@
-// The experts' products on CUDA cores, for fp32 and for widths or pointers
-// the tensor-core kernels do not take.  Every product is a tile of 16 R x 64
+// The experts' products on CUDA cores, for fp32 and GMM_FLAG_FORCE_SIMT.  Every product is a tile of 16 R x 64
 // with an R x 4 micro tile per thread (forward calls of a few rows per expert: a
 // dot product per warp), fp32 throughout; what one product hands to the next
 // stays fp32 in the workspace.  Bound by the FMA pipes and what
@@ -367,9 +366,10 @@ __device__ __forceinline__ void dots(float (&sums)[kFewRows], const A &opa, int 
 }
 
 // One layer where the experts' segments hold few rows: a warp takes one output
-// column, reads that row of the weight once, coalesced, and multiplies it with
-// four points' rows at a time (from L1: the block's eight warps share them).
-// Bound by the weights' read for a row or two, then by L1.
+// column of a tile and multiplies that row of the weight, read coalesced, with
+// four points' rows at a time (from L1: the block's eight warps share them; the
+// weight's row is read again for every four).  Bound by the weights' read for
+// a row or two, then by L1.
 template <typename T, int ACT, bool GATED, bool SECOND, bool V>
 __global__ void __launch_bounds__(256) simt_few_kernel(ExpCall c) {
     exp_wait();
@@ -560,7 +560,11 @@ static int64_t tiles_of(int64_t n, int w) { return (n + w - 1) / w; }
 // Mean rows per expert up to which a forward call takes simt_few_kernel.  One
 // dense 1024-4096 map: 1 point 4.9 us against 52 in tiles, 8 points 10 against
 // 53; 16 points, r = 4 of 64 experts 512-1024-512 67 against 176; with 9 rows
-// an expert (300 points, r = 2 of 64 experts 512-512-512) 137 against 125.
+// an expert (300 points, r = 2 of 64 experts 512-512-512) 137 against 125.  The
+// mean says nothing of the lengths: with 8 rows an expert, 512-512-512, 64
+// experts take 90 us against 122 in tiles when used evenly, 193 against 123
+// when half of the points are one expert's, 167 against 87 when all are; 256
+// experts 321 against 378, 458 against 423 and 331 against 122.
 constexpr int64_t kFewMean = 8;
 
 // Rows per thread of a product over the points' rows, with `cols` column

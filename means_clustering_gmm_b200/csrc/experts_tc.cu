@@ -650,6 +650,11 @@ __global__ void __launch_bounds__(kThreads, 1) exp_tc_kernel(const __grid_consta
                         x[i] = __fmul2_rn(gq, du);
                         if constexpr (KIND == kDaMlp) hs[i] = __fmul2_rn(splat(g), fu);
                     }
+                    // dresp: fp32, of accumulators that truncate, which costs 1e-9
+                    // of q and of the pre-activations with each contraction index.
+                    // Adding pieces of the contraction in fp32 here instead would
+                    // take 96 registers a thread, all there are, and TMEM has no
+                    // columns left for such sums beside a gated tile's.
                     part += sum.x + sum.y;
                     // rows past the segment are zeros: the weight gradients
                     // contract over them

@@ -1,8 +1,8 @@
 // Inline-PTX wrappers for the sm_100a tensor-core kernels: mbarriers with
-// bounded waits, 1-D bulk copies (cp.async.bulk, no multicast), TMEM
-// allocation, tcgen05.mma (kind::f16, cta_group::1), tcgen05.commit,
-// tcgen05.ld/st, cluster rank / DSMEM stores / remote mbarrier arrivals, and
-// the shared-memory / instruction descriptors.
+// bounded waits, 1-D bulk copies and 2-D / 3-D tensor-map copies and prefetches
+// (no multicast), TMEM allocation, tcgen05.mma (kind::f16) and tcgen05.commit
+// of one CTA and of a pair, tcgen05.ld/st, cluster rank / DSMEM stores / remote
+// mbarrier arrivals, and the shared-memory / instruction descriptors.
 //
 // Descriptor formats follow the PTX ISA's tcgen05 "shared memory descriptor"
 // and "instruction descriptor" tables (bit positions cross-checked against
