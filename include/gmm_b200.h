@@ -487,8 +487,8 @@ size_t gmm_expert_workspace_size(const gmm_expert_shape *shape, int backward, ui
  *   Y may be the residual's own buffer; it may not overlap another input.
  *   flags    0, or GMM_FLAG_FORCE_SIMT (CUDA-core kernels).
  * Errors: GMM_ERR_INVALID_ARG for NULL or misaligned pointers (X, weights,
- * Y, dY and the gradients of X and the weights 16 bytes, the workspace 256,
- * the others their element), invalid shapes and flags, a short workspace:
+ * Y, dY and the gradients of X and the weights 16 bytes where their rows are
+ * whole 16-byte units, the workspace 256, all others their element), invalid shapes and flags, a short workspace:
  * nothing is launched then.  GMM_ERR_CUDA if a launch fails: those before it
  * in the call still run, and what the call writes is undefined.
  */

@@ -147,12 +147,16 @@ ExpCall make_call(const ExpShape &p, const Layout &L, void *ws, const int32_t *i
 
 bool known_flags(uint32_t flags) { return (flags & ~(uint32_t)GMM_FLAG_FORCE_SIMT) == 0; }
 
-// The checks the four entry points share; `big` arrays are 16-byte aligned,
-// `small` ones to their element.
+// The checks the four entry points share.  `big` arrays are 16-byte aligned
+// where their rows are whole 16-byte units; others are read and written element by
+// element (the copies of 16-bit types, the CUDA cores' scalar form) and aligned
+// to that, as `small` ones are.
 struct Checks {
     bool ok = true;
     size_t elem;
-    void big(const void *p) { ok = ok && p && aligned(p, 16); }
+    void big(const void *p, int width) {
+        ok = ok && p && aligned(p, width * elem % 16 == 0 ? 16 : elem);
+    }
     void small(const void *p, size_t a) { ok = ok && (!p || aligned(p, a)); }
     void routing(const gmm_expert_shape *s, const int32_t *ids, const float *resp) {
         ok = ok && (ids != nullptr) == (s->r > 0) && (s->r > 0 || !resp);
@@ -266,10 +270,10 @@ gmm_status forward(const gmm_expert_shape *shape, bool mlp, const void *X, const
     const Layout L = layout_of(q, false, path);
     Checks k;
     k.elem = p.dt == GMM_F32 ? 4 : 2;
-    k.big(X);
-    k.big(W1);
-    if (mlp) k.big(W2);
-    k.big(Y);
+    k.big(X, p.d);
+    k.big(W1, p.d);
+    if (mlp) k.big(W2, p.h);
+    k.big(Y, p.o);
     k.small(b1, k.elem);
     k.small(b2, k.elem);
     k.small(residual, k.elem);
@@ -302,14 +306,14 @@ gmm_status backward(const gmm_expert_shape *shape, bool mlp, const void *dY, con
     const Layout L = layout_of(q, true, path);
     Checks k;
     k.elem = p.dt == GMM_F32 ? 4 : 2;
-    k.big(dY);
-    k.big(X);
-    k.big(W1);
-    k.big(dX);
-    k.big(dW1);
+    k.big(dY, p.o);
+    k.big(X, p.d);
+    k.big(W1, p.d);
+    k.big(dX, p.d);
+    k.big(dW1, p.d);
     if (mlp) {
-        k.big(W2);
-        k.big(dW2);
+        k.big(W2, p.h);
+        k.big(dW2, p.h);
     }
     k.small(b1, k.elem);
     k.small(b2, k.elem);

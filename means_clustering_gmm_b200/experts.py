@@ -17,8 +17,8 @@ device (two captured graphs that may run at once need one each).  ``stream``
 (default: the current one of X's device) is where a call runs and its outputs
 belong; its inputs have to be ready there.  Arrays given to a call with
 ``stream`` may be dropped at once: their memory is kept until it is done.
-Bases of X, dY, the weights and ``out`` must be 16-byte aligned (whole tensors
-are).  An id at or above K is skipped and recorded: ``gmm_last_error(ws)``
+Bases of X, dY, the weights and ``out`` must be 16-byte aligned where their rows
+are whole 16-byte units (whole tensors are).  An id at or above K is skipped and recorded: ``gmm_last_error(ws)``
 reports GMM_ERR_RANGE.
 """
 from __future__ import annotations

@@ -280,3 +280,28 @@ def test_result_may_replace_the_residual_at_odd_widths(N, r, h, dtype):
 def test_many_experts(K, N, r, dtype):
     """The most experts, and both sides of the one-block routing's limit."""
     check(inputs(93, N, 16, 0, 8, K, r, dtype, cut=0.1), "silu")
+
+
+@pytest.mark.parametrize("N,d,h,o,r,dtype,flags", [
+    (300, 33, 21, 65, 2, "bf16", 0), (40, 31, 0, 27, 1, "f16", 0), (3, 33, 40, 65, 2, "bf16", 0),
+    (700, 64, 61, 50, 1, "f16", 0), (300, 33, 21, 65, 2, "f32", 0), (20, 30, 0, 26, 1, "f32", 0),
+    (300, 64, 0, 27, 0, "f32", 0), (300, 33, 21, 65, 2, "bf16", gmm.GMM_FLAG_FORCE_SIMT),
+    (300, 50, 0, 64, 2, "f16", gmm.GMM_FLAG_FORCE_SIMT)])
+def test_odd_widths_at_any_element(N, d, h, o, r, dtype, flags):
+    """Arrays whose rows are not whole 16-byte units may start at any element
+    (slices of rows do), the others at 16 bytes."""
+    s = inputs(95, N, d, h, o, 4 if r else 1, r, dtype, res=True)
+    want = forward(cuda(s), "silu", flags=flags)[0], backward(cuda(s), "silu", flags=flags)[0]
+    size = s["x"].element_size()
+
+    def shifted(t, k=1):
+        k = k if t.shape[-1] * size % 16 else 16 // size
+        room = torch.empty(t.numel() + k, dtype=t.dtype, device="cuda")
+        return room[k:].view(t.shape).copy_(t)
+
+    c = {k: shifted(t) if isinstance(t, torch.Tensor) and k not in ("ids", "resp") else
+         t.cuda() if isinstance(t, torch.Tensor) else t for k, t in s.items()}
+    out = shifted(torch.zeros(N, o, dtype=DT[dtype]), 3)
+    assert torch.equal(forward(c, "silu", flags=flags, out=out)[0], want[0])
+    got = backward(c, "silu", flags=flags)[0]
+    assert all(torch.equal(got[k], want[1][k]) for k in want[1])
