@@ -38,15 +38,17 @@ def keep_for(stream, *tensors) -> None:
             t.record_stream(stream)
 
 
-def _on(stream, call, *args, **kw):
-    """call(*args, **kw) with `stream` current, so that what it allocates and
+def _on(stream, call, *args):
+    """call(*args) with `stream` current, so that what it allocates and
     prepares is that stream's.  The memory of what is given is kept until the
     stream has used it, that of what is returned until the caller's stream has."""
     here = torch.cuda.current_stream(stream.device)
-    with torch.cuda.stream(stream):
-        out = call(*args, **kw)
-    tensors = [a.buf if isinstance(a, Workspace) else a for a in (*args, *kw.values())]
-    keep_for(stream, *(t for t in tensors if isinstance(t, torch.Tensor) and t.is_cuda))
+    tensors = [a.buf if isinstance(a, Workspace) else a for a in args]
+    try:
+        with torch.cuda.stream(stream):
+            out = call(*args)
+    finally:   # (a failed call may have launched a part of it)
+        keep_for(stream, *(t for t in tensors if isinstance(t, torch.Tensor) and t.is_cuda))
     keep_for(here, *(t for t in out if isinstance(t, torch.Tensor) and t.is_cuda))
     return out
 

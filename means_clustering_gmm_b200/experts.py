@@ -167,10 +167,11 @@ class _Call:
             self.guard.__exit__(*exc)
 
     def run(self, name, fn, flags, *args):
-        check(name, fn(self.shape, *[None if t is None else t.data_ptr() for t in args],
-                       self.ws.ptr, self.ws.nbytes, int(flags), self.stream))
-        if self.side is not None:
+        status = fn(self.shape, *[None if t is None else t.data_ptr() for t in args], self.ws.ptr,
+                    self.ws.nbytes, int(flags), self.stream)
+        if self.side is not None:   # (a failed call may have launched a part of it)
             keep_for(self.side, self.ws.buf, *args)
+        check(name, status)
 
 
 def _like(t):
